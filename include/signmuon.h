@@ -331,6 +331,113 @@ signmuon_status signmuon_momentum_norm_noalloc(const signmuon_shape* shapes, int
                                                float* const* mom, float beta, void* const* x_bf16,
                                                float* inv_norm, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Per-worker gradients of a token model around its hidden matrices.
+ * The paper has no counterpart: its workers are given their gradients.
+ *
+ * A batch of `rows` token rows holds the rows of all workers: worker m owns
+ * rows [row_begin[m], row_begin[m + 1]) (host array of n_workers + 1
+ * non-decreasing offsets, row_begin[0] = 0, row_begin[n_workers] = rows; a
+ * worker may own none).  One backward call over the whole batch writes every
+ * worker's own gradient, G^(m) of step 1, into n_workers buffers given as a
+ * host array of device pointers: the grad arguments of signmuon_momentum_norm
+ * and signmuon_momentum_sign for that matrix.
+ *
+ * Unlike the step's own buffers, row buffers here take any row stride
+ * ld >= cols (in elements) and any address that is a multiple of the element
+ * size; 16-byte aligned rows of a multiple of 16 bytes run fastest.  Only the
+ * workspace has to be 256-byte aligned.  Rows of embeddings and layer norms
+ * have at most 2^20 columns (else SIGNMUON_ERR_UNSUPPORTED).  rows = 0 is allowed (row pointers may
+ * then be NULL).  Sums are taken in fp32 in an order fixed by the shapes and
+ * ids, and rounded once, to nearest, to the output's type: results are
+ * bit-reproducible.  Outputs must not overlap inputs unless stated.
+ * ---------------------------------------------------------------------- */
+
+/* Embedding lookup: y[t, :] = scale * table[ids[t], :], zero where ids[t] is
+ * outside [0, table.rows) (padding).
+ * table: device [rows, ld_table] of table_dtype; ids: device int32 (ids_int64
+ * == 0) or int64 [n_tokens]; y: device [n_tokens, ld_y] of y_dtype. */
+signmuon_status signmuon_embedding_forward(signmuon_shape table_shape, signmuon_dtype table_dtype,
+                                           const void* table, int64_t ld_table, int64_t n_tokens,
+                                           int ids_int64, const void* ids, float scale,
+                                           signmuon_dtype y_dtype, void* y, int64_t ld_y, void* stream);
+
+/* The table's gradient per worker:
+ *   grad[m][v, :] = scale * sum over worker m's tokens t with ids[t] == v of dy[t, :]
+ * (accumulate == 0: every row is written, zero where no token names it), or
+ * that sum added to grad[m][v, :] (accumulate != 0: only rows that a token
+ * names are touched; one rounding of old + sum).  Tokens outside the table
+ * give nothing.  Each worker's tokens are sorted by id and added in token
+ * order.
+ * dy: device [row_begin[n_workers], ld_dy] of dy_dtype; grad: host array of
+ * n_workers device pointers, [rows, cols] of grad_dtype, row stride cols; no
+ * two of them overlap.  At most 2^31 - 1 tokens.
+ * workspace: device, >= signmuon_embedding_backward_workspace_bytes(...). */
+size_t signmuon_embedding_backward_workspace_bytes(signmuon_shape table_shape, int n_workers,
+                                                   const int64_t* row_begin);
+signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_workers,
+                                            const int64_t* row_begin, int ids_int64, const void* ids,
+                                            signmuon_dtype dy_dtype, const void* dy, int64_t ld_dy,
+                                            float scale, int accumulate, signmuon_dtype grad_dtype,
+                                            void* const* grad, void* workspace, size_t ws_bytes,
+                                            void* stream);
+
+/* Layer norm over rows of `cols` elements:
+ *   mean = sum(x) / cols, rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ * x: device [rows, ld_x] and y: device [rows, ld_y] of x_dtype (y may be x
+ * itself, with the same stride); weight, bias: device [cols] of w_dtype (bias
+ * may be NULL); mean, rstd: device fp32 [rows], what the backward call needs.
+ * eps >= 0. */
+signmuon_status signmuon_layer_norm_forward(int64_t rows, int32_t cols, signmuon_dtype x_dtype,
+                                            const void* x, int64_t ld_x, signmuon_dtype w_dtype,
+                                            const void* weight, const void* bias, float eps, void* y,
+                                            int64_t ld_y, float* mean, float* rstd, void* stream);
+
+/* Its gradients, with xh = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - sum(g) / cols - xh * sum(g * xh) / cols)
+ *   dweight[m] = sum over worker m's rows of dy * xh,  dbias[m] = sum of dy
+ * dx: device [rows, ld_dx] of x_dtype (dx may be dy itself, with the same
+ * stride); dweight, dbias: host arrays of n_workers device pointers, [cols]
+ * of w_dtype (dbias may be NULL).
+ * workspace: device, >= signmuon_layer_norm_backward_workspace_bytes(...). */
+size_t signmuon_layer_norm_backward_workspace_bytes(int32_t cols, int n_workers, const int64_t* row_begin);
+signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const int64_t* row_begin,
+                                             signmuon_dtype x_dtype, const void* dy, int64_t ld_dy,
+                                             const void* x, int64_t ld_x, signmuon_dtype w_dtype,
+                                             const void* weight, const float* mean, const float* rstd,
+                                             void* dx, int64_t ld_dx, void* const* dweight,
+                                             void* const* dbias, void* workspace, size_t ws_bytes,
+                                             void* stream);
+
+/* Distillation from a teacher's top logits, and its gradient.
+ * Entry k of row n is present where 0 <= top_ids[n, k] < vocab and its logit
+ * u = top_logits[n, k] is not -inf.  With T = temperature,
+ *   p = softmax(u / T) over the row's present entries,
+ *   q = softmax(logits[n, :] / T) over the vocabulary,
+ *   row_loss[n] = T^2 * sum over present entries of p * (log p - log q[id]),
+ * where an entry whose p underflows to zero counts nothing; an id that comes
+ * up more than once holds the sum of its entries' p.  A row without present
+ * entries is ignored: loss 0, gradient 0, its logits are not looked at.  With n_m the number of worker m's rows that
+ * are not ignored,
+ *   loss[m] = sum of worker m's row losses / max(n_m, 1)
+ *   dlogits[n, :] = grad_scale * d loss[m] / d logits[n, :]
+ *                 = grad_scale * T * (q - p) / n_m
+ * logits: device [rows, ld] of dtype; top_ids: device int32 or int64 [rows,
+ * top], top_logits: device [rows, top] of top_dtype, both contiguous;
+ * 1 <= top <= 1024; row_loss: device fp32 [rows]; loss: device fp32
+ * [n_workers]; dlogits: device [rows, ld_d] of dtype, NULL for the losses
+ * alone (it may be logits itself, with the same stride).
+ * temperature > 0 and finite.
+ * workspace: device, >= signmuon_distill_workspace_bytes(...). */
+size_t signmuon_distill_workspace_bytes(int64_t rows, int top);
+signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_t* row_begin,
+                                      signmuon_dtype dtype, const void* logits, int64_t ld, int top,
+                                      int ids_int64, const void* top_ids, signmuon_dtype top_dtype,
+                                      const void* top_logits, float temperature, float grad_scale,
+                                      float* loss, float* row_loss, void* dlogits, int64_t ld_d,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,9 @@ EXPORTS = (
     "signmuon_sign_pack", "signmuon_vote_workspace_bytes", "signmuon_vote_update",
     "signmuon_momentum_norm_noalloc", "signmuon_last_error_string",
     "signmuon_spectral_workspace_bytes", "signmuon_spectral_norm", "signmuon_momentum_sign",
+    "signmuon_embedding_forward", "signmuon_embedding_backward_workspace_bytes", "signmuon_embedding_backward",
+    "signmuon_layer_norm_forward", "signmuon_layer_norm_backward_workspace_bytes", "signmuon_layer_norm_backward",
+    "signmuon_distill_workspace_bytes", "signmuon_distill_loss",
 )
 
 
@@ -61,6 +64,8 @@ _PP = ctypes.POINTER(ctypes.c_void_p)
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _F = ctypes.c_float
+_I64 = ctypes.c_int64
+_I64P = ctypes.POINTER(ctypes.c_int64)
 
 _SIGS = {
     "signmuon_status_string": (ctypes.c_char_p, [_I]),
@@ -87,6 +92,16 @@ _SIGS = {
     "signmuon_momentum_norm_noalloc": (_I, [ctypes.POINTER(Shape), _I, _I, _I, _PP, _PP, _F, _PP, _P, _P]),
     "signmuon_vote_update": (_I, [ctypes.POINTER(Shape), _I, _I, _I, _PP, _I, _PP, _F, _PP, _P, _P,
                                   _P, _SZ, _P]),
+    "signmuon_embedding_forward": (_I, [Shape, _I, _P, _I64, _I64, _I, _P, _F, _I, _P, _I64, _P]),
+    "signmuon_embedding_backward_workspace_bytes": (_SZ, [Shape, _I, _I64P]),
+    "signmuon_embedding_backward": (_I, [Shape, _I, _I64P, _I, _P, _I, _P, _I64, _F, _I, _I, _PP, _P, _SZ, _P]),
+    "signmuon_layer_norm_forward": (_I, [_I64, ctypes.c_int32, _I, _P, _I64, _I, _P, _P, _F, _P, _I64, _P, _P, _P]),
+    "signmuon_layer_norm_backward_workspace_bytes": (_SZ, [ctypes.c_int32, _I, _I64P]),
+    "signmuon_layer_norm_backward": (_I, [ctypes.c_int32, _I, _I64P, _I, _P, _I64, _P, _I64, _I, _P, _P, _P, _P, _I64,
+                                          _PP, _PP, _P, _SZ, _P]),
+    "signmuon_distill_workspace_bytes": (_SZ, [_I64, _I]),
+    "signmuon_distill_loss": (_I, [ctypes.c_int32, _I, _I64P, _I, _P, _I64, _I, _I, _P, _I, _P, _F, _F, _P, _P, _P, _I64,
+                                   _P, _SZ, _P]),
 }
 
 _lib = None
@@ -249,3 +264,60 @@ def signmuon_momentum_norm_noalloc(shapes, n_workers, grad_dtype, grad, mom, bet
                                                _ptrs(grad), _ptrs(mom), beta, _ptrs(x_bf16), inv_norm,
                                                stream)
     _check("signmuon_momentum_norm_noalloc", st)
+
+
+def _offsets(row_begin):
+    """Row offsets (a sequence, or an int64 array made by an earlier call) as
+    a C array; its length is the number of workers + 1."""
+    return row_begin if isinstance(row_begin, ctypes.Array) else (ctypes.c_int64 * len(row_begin))(*row_begin)
+
+
+def signmuon_embedding_forward(table_shape, table_dtype, table, ld_table, n_tokens, ids_int64, ids, scale, y_dtype, y,
+                               ld_y, stream=0) -> None:
+    st = load().signmuon_embedding_forward(Shape(*table_shape), table_dtype, table, ld_table, n_tokens, int(bool(ids_int64)),
+                                           ids, scale, y_dtype, y, ld_y, stream)
+    _check("signmuon_embedding_forward", st)
+
+
+def signmuon_embedding_backward_workspace_bytes(table_shape, row_begin) -> int:
+    return load().signmuon_embedding_backward_workspace_bytes(Shape(*table_shape), len(row_begin) - 1,
+                                                              _offsets(row_begin))
+
+
+def signmuon_embedding_backward(table_shape, row_begin, ids_int64, ids, dy_dtype, dy, ld_dy, scale, accumulate, grad_dtype,
+                                grad, workspace, ws_bytes, stream=0) -> None:
+    st = load().signmuon_embedding_backward(Shape(*table_shape), len(row_begin) - 1, _offsets(row_begin),
+                                            int(bool(ids_int64)), ids, dy_dtype, dy, ld_dy, scale, int(bool(accumulate)),
+                                            grad_dtype, _ptrs(grad), workspace, ws_bytes, stream)
+    _check("signmuon_embedding_backward", st)
+
+
+def signmuon_layer_norm_forward(rows, cols, x_dtype, x, ld_x, w_dtype, weight, bias, eps, y, ld_y, mean, rstd,
+                                stream=0) -> None:
+    st = load().signmuon_layer_norm_forward(rows, cols, x_dtype, x, ld_x, w_dtype, weight, bias, eps, y, ld_y, mean, rstd,
+                                            stream)
+    _check("signmuon_layer_norm_forward", st)
+
+
+def signmuon_layer_norm_backward_workspace_bytes(cols, row_begin) -> int:
+    return load().signmuon_layer_norm_backward_workspace_bytes(cols, len(row_begin) - 1, _offsets(row_begin))
+
+
+def signmuon_layer_norm_backward(cols, row_begin, x_dtype, dy, ld_dy, x, ld_x, w_dtype, weight, mean, rstd, dx, ld_dx,
+                                 dweight, dbias, workspace, ws_bytes, stream=0) -> None:
+    st = load().signmuon_layer_norm_backward(cols, len(row_begin) - 1, _offsets(row_begin), x_dtype, dy, ld_dy, x, ld_x,
+                                             w_dtype, weight, mean, rstd, dx, ld_dx, _ptrs(dweight), _ptrs(dbias),
+                                             workspace, ws_bytes, stream)
+    _check("signmuon_layer_norm_backward", st)
+
+
+def signmuon_distill_workspace_bytes(rows, top) -> int:
+    return load().signmuon_distill_workspace_bytes(rows, top)
+
+
+def signmuon_distill_loss(vocab, row_begin, dtype, logits, ld, top, ids_int64, top_ids, top_dtype, top_logits, temperature,
+                          grad_scale, loss, row_loss, dlogits, ld_d, workspace, ws_bytes, stream=0) -> None:
+    st = load().signmuon_distill_loss(vocab, len(row_begin) - 1, _offsets(row_begin), dtype, logits, ld, top,
+                                      int(bool(ids_int64)), top_ids, top_dtype, top_logits, temperature, grad_scale, loss,
+                                      row_loss, dlogits, ld_d, workspace, ws_bytes, stream)
+    _check("signmuon_distill_loss", st)

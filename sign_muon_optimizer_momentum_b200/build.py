@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsignmuon.so")
-SOURCES = ["api.cu", "elementwise.cu", "ns_gemm.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "elementwise.cu", "ns_gemm.cu", "noalloc.cu", "embedding.cu", "layer_norm.cu", "distill.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,583 @@
+// Embedding lookup with scaling, and the table's gradient per worker.
+//
+//   forward    y[t] = s W[id_t]                     (0 for ids outside the table)
+//   backward   G^(m)[v] = s sum_{t of worker m, id_t = v} dy[t]
+//
+// The lookup reads the rows that the ids name and writes y.  The gradient
+// reads dy once and writes n_workers whole tables, nearly all zeros for a
+// large vocabulary, so its floor is those writes.  It runs without atomics,
+// in an order fixed by the ids:
+//   1. sort   Each worker's (id, token) pairs are sorted by id in tiles of
+//             kTile, a block a tile, in shared memory (stable counting passes
+//             of up to 9 bits).  The other blocks of the launch meanwhile fill
+//             the tables with zeros: the sort is bound by latency and takes
+//             few SMs, the fill is bound by HBM.
+//   2. merge  Only for workers of more than one tile: each pair's place is its
+//             place in its own run plus the smaller pairs of the other runs,
+//             found by binary search, kFan runs at a time.
+//   3. reduce A warp takes kChunk consecutive sorted pairs and a slab of
+//             columns, adds the rows of each run of equal ids in registers and
+//             writes the runs that lie within the chunk.  What a run that
+//             crosses a chunk's ends has there is left as a partial row.
+//   4. join   The chunk where such a run begins adds its partial rows and
+//             writes the row; long runs (frequent tokens) by a whole block.
+#include "layers.cuh"
+
+using namespace signmuon;
+
+namespace {
+
+constexpr int kLookupThreads = 256;
+constexpr int kLookupVecs = 4;       // vectors a lane loads of a row
+constexpr int kSortThreads = 1024;
+constexpr int kSortItems = 4;        // pairs a thread
+constexpr int kTile = kSortThreads * kSortItems;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 9;
+constexpr int kDigits = 1 << kDigitBits;
+constexpr int kFan = 32;             // runs merged at a time
+constexpr int kMergeThreads = 256;
+constexpr int kChunk = 32;           // sorted pairs a warp of the reduction takes
+constexpr int kLaneCols = 8;         // columns of a lane's slab
+constexpr int kSlab = 32 * kLaneCols;
+constexpr int kReduceThreads = 256;
+constexpr int kJoinChunks = 8;       // chunks (warps) a block of the join looks at
+constexpr int kLongRun = 16;         // chunks from which a whole block adds a run
+
+// ----------------------------------------------------------------- lookup
+// lanes (a power of two) lanes take kLookupVecs vectors each of a token's
+// row; blockIdx.y is the segment of rows that are longer than that.
+template <typename TW, typename TY, int VEC>
+__global__ void __launch_bounds__(kLookupThreads)
+lookup_kernel(const TW* __restrict__ table, int64_t ld_table, int32_t vocab, int32_t cols, int64_t n_tokens,
+              const void* __restrict__ ids, int wide, float scale, TY* __restrict__ y, int64_t ld_y, int lanes) {
+  const int64_t token = (int64_t)blockIdx.x * (kLookupThreads / lanes) + threadIdx.x / lanes;
+  if (token >= n_tokens) return;
+  const int64_t id = load_id(ids, token, wide);
+  const bool in = id >= 0 && id < vocab;
+  const TW* src = table + (in ? id : 0) * ld_table;
+  const int first = (blockIdx.y * lanes * kLookupVecs + threadIdx.x % lanes) * VEC;
+  typename RawVec<TW, VEC>::type raw[kLookupVecs];
+#pragma unroll
+  for (int i = 0; i < kLookupVecs; ++i) {
+    const int col = first + i * lanes * VEC;
+    if (in && col < cols) raw[i] = __ldg(reinterpret_cast<const typename RawVec<TW, VEC>::type*>(src + col));
+  }
+#pragma unroll
+  for (int i = 0; i < kLookupVecs; ++i) {
+    const int col = first + i * lanes * VEC;
+    if (col < cols) {
+      float v[VEC];
+      if (in) unpack(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = in ? v[j] * scale : 0.f;
+      store_stream<TY, VEC>(y + token * ld_y + col, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------ sort and fill
+struct Fill {
+  WorkerPtrs grad;
+  int64_t bytes;  // of one table; 0: nothing to fill
+};
+
+__device__ void fill_zero(const Fill& f, int n_workers, int block, int blocks) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int m = 0; m < n_workers; ++m) {
+    uint8_t* p = static_cast<uint8_t*>(f.grad.p[m]);
+    // The ends that are not whole 16 bytes, two bytes at a time.
+    const int64_t head = min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15), f.bytes);
+    const int64_t n16 = (f.bytes - head) / 16, tail = head + n16 * 16;
+    if (block == 0) {
+      for (int64_t i = threadIdx.x * 2; i < head; i += kSortThreads * 2) *reinterpret_cast<uint16_t*>(p + i) = 0;
+      for (int64_t i = tail + threadIdx.x * 2; i < f.bytes; i += kSortThreads * 2) *reinterpret_cast<uint16_t*>(p + i) = 0;
+    }
+    uint4* q = reinterpret_cast<uint4*>(p + head);
+    for (int64_t i = (int64_t)block * kSortThreads + threadIdx.x; i < n16; i += (int64_t)blocks * kSortThreads) __stcs(q + i, zero);
+  }
+}
+
+// Blocks 0 .. tiles.begin[n_workers] - 1 sort a tile each, the rest fill.
+// Keys are ids; an id outside the table gets the key `vocab` and sorts last.
+__global__ void __launch_bounds__(kSortThreads)
+sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks tiles, int n_workers,
+                  const void* __restrict__ ids, int wide, uint32_t vocab, int passes, int bits, uint32_t* __restrict__ out_key,
+                  uint32_t* __restrict__ out_tok, const __grid_constant__ Fill fill) {
+  __shared__ uint32_t s_key[kTile];
+  __shared__ uint16_t s_tok[kTile];
+  extern __shared__ uint16_t s_count[];  // [kSortWarps][kDigits]
+  __shared__ uint32_t s_digit[kDigits];  // first place of each digit
+  __shared__ uint32_t s_warp[kSortWarps];
+  const int n_tiles = tiles.begin[n_workers];
+  if ((int)blockIdx.x >= n_tiles) {
+    fill_zero(fill, n_workers, blockIdx.x - n_tiles, gridDim.x - n_tiles);
+    return;
+  }
+  const int m = worker_of_block(tiles, n_workers, blockIdx.x);
+  const int64_t base = rows.begin[m] + (int64_t)(blockIdx.x - tiles.begin[m]) * kTile;
+  const int n = (int)min((int64_t)kTile, rows.begin[m + 1] - base);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int first = warp * 32 * kSortItems + lane;  // this thread's items: first + 32 j
+  uint32_t key[kSortItems], tok[kSortItems];
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    const int i = first + 32 * j;
+    int64_t id = -1;
+    if (i < n) id = load_id(ids, base + i, wide);
+    key[j] = id >= 0 && id < (int64_t)vocab ? (uint32_t)id : vocab;
+    tok[j] = i;
+  }
+  const uint32_t mask = (1u << bits) - 1;
+  uint16_t* count = s_count + warp * kDigits;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * bits;
+    for (int i = lane; i < kDigits; i += 32) count[i] = 0;
+    __syncwarp();
+    uint32_t rank[kSortItems];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+      const uint32_t d = key[j] >> shift & mask;
+      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      const uint32_t before = peers & ((1u << lane) - 1);
+      const uint32_t seen = count[d];
+      rank[j] = seen + __popc(before);
+      __syncwarp();
+      if (before == 0) count[d] = (uint16_t)(seen + __popc(peers));
+      __syncwarp();
+    }
+    __syncthreads();
+    // Counts to places: by digit, within a digit by warp.
+    uint32_t total = 0;
+    if (threadIdx.x < kDigits) {
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = s_count[w * kDigits + threadIdx.x];
+        s_count[w * kDigits + threadIdx.x] = (uint16_t)total;
+        total += c;
+      }
+    }
+    uint32_t scan = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) s_warp[warp] = scan;
+    __syncthreads();
+    if (threadIdx.x < kDigits) {
+      uint32_t lower = 0;
+      for (int w = 0; w < warp; ++w) lower += s_warp[w];
+      s_digit[threadIdx.x] = lower + scan - total;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+      const uint32_t d = key[j] >> shift & mask;
+      const uint32_t at = s_digit[d] + count[d] + rank[j];
+      s_key[at] = key[j];
+      s_tok[at] = (uint16_t)tok[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) key[j] = s_key[first + 32 * j], tok[j] = s_tok[first + 32 * j];
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    const int i = first + 32 * j;
+    if (i < n) out_key[base + i] = key[j], out_tok[base + i] = (uint32_t)(base + tok[j]);
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// Runs of `run` sorted pairs of each worker, kFan at a time, to runs of
+// kFan * run.  Equal keys keep the runs' order.
+__global__ void __launch_bounds__(kMergeThreads)
+merge_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks blocks, int n_workers, int64_t run,
+             const uint32_t* __restrict__ key, const uint32_t* __restrict__ tok, uint32_t* __restrict__ out_key,
+             uint32_t* __restrict__ out_tok) {
+  const int m = worker_of_block(blocks, n_workers, blockIdx.x);
+  const int64_t n = rows.begin[m + 1] - rows.begin[m];
+  const int64_t p = (int64_t)(blockIdx.x - blocks.begin[m]) * kMergeThreads + threadIdx.x;
+  if (p >= n) return;
+  key += rows.begin[m];
+  const uint32_t k = key[p];
+  const int64_t mine = p / run, group = mine / kFan * kFan;
+  int64_t place = group * run + (p - mine * run);
+#pragma unroll 4
+  for (int i = 0; i < kFan; ++i) {
+    const int64_t other = group + i, begin = other * run;
+    if (other == mine || begin >= n) continue;
+    // Pairs of the other run that go before: keys below k, and equal ones of
+    // an earlier run.
+    const uint32_t below = k + (other < mine ? 1u : 0u);
+    int64_t lo = begin, hi = min(begin + run, n);
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (key[mid] < below) lo = mid + 1;
+      else hi = mid;
+    }
+    place += lo - begin;
+  }
+  out_key[rows.begin[m] + place] = k;
+  out_tok[rows.begin[m] + place] = tok[rows.begin[m] + p];
+}
+
+// ----------------------------------------------------------------- reduce
+struct ReduceArgs {
+  const uint32_t* key;
+  const uint32_t* tok;
+  const void* dy;
+  int64_t ld_dy;
+  float* part;  // [chunks][2][cols]: what the run from the chunk before, and the one into the next, have here
+  uint32_t vocab;
+  int32_t cols, n_workers, accumulate;
+  float scale;
+};
+
+// One chunk of a worker's sorted pairs.
+struct Chunk {
+  int64_t begin;   // of the pairs
+  int n;           // pairs in the table (the others sort last)
+  uint32_t key;    // this lane's
+  uint32_t ends;   // bit j: a run ends at pair j
+  bool from_before, into_next;
+};
+__device__ __forceinline__ Chunk chunk_at(const ReduceArgs& a, const WorkerRows& rows, const WorkerBlocks& chunks, int m,
+                                          int chunk) {
+  Chunk c;
+  const int lane = threadIdx.x & 31;
+  c.begin = rows.begin[m] + (int64_t)(chunk - chunks.begin[m]) * kChunk;
+  const int64_t end = rows.begin[m + 1];
+  const bool in = c.begin + lane < end;
+  c.key = in ? a.key[c.begin + lane] : a.vocab;
+  // The neighbours' keys; vocab where there is none, which equals no key here.
+  uint32_t edge = a.vocab;
+  if (lane == 0 && c.begin > rows.begin[m]) edge = a.key[c.begin - 1];
+  if (lane == 31 && c.begin + kChunk < end) edge = a.key[c.begin + kChunk];
+  c.n = __popc(__ballot_sync(0xffffffffu, c.key < a.vocab));
+  uint32_t after = __shfl_down_sync(0xffffffffu, c.key, 1);
+  if (lane == 31) after = edge;
+  c.ends = __ballot_sync(0xffffffffu, c.key < a.vocab && c.key != after);
+  const uint32_t joins = __ballot_sync(0xffffffffu, c.key < a.vocab && c.key == edge);
+  c.from_before = joins & 1u;
+  c.into_next = joins >> 31;
+  return c;
+}
+
+template <typename TG, int VEC>
+__device__ __forceinline__ void write_grad(TG* row, int col0, int cols, int accumulate, float scale, const float (&acc)[kLaneCols]) {
+#pragma unroll
+  for (int c = 0; c < kLaneCols / VEC; ++c) {
+    const int col = col0 + c * 32 * VEC;
+    if (col < cols) {
+      float v[VEC];
+      if (accumulate) unpack(*reinterpret_cast<const typename RawVec<TG, VEC>::type*>(row + col), v);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = accumulate ? fmaf(acc[c * VEC + j], scale, v[j]) : acc[c * VEC + j] * scale;
+      store_vec<TG, VEC>(row + col, v);
+    }
+  }
+}
+
+template <typename TD, typename TG, int VEC>
+__global__ void __launch_bounds__(kReduceThreads)
+reduce_kernel(const ReduceArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks chunks,
+              const __grid_constant__ WorkerPtrs grad) {
+  constexpr int kVecs = kLaneCols / VEC, kBatch = 4;
+  const int lane = threadIdx.x & 31, chunk = blockIdx.x * (kReduceThreads / 32) + threadIdx.x / 32;
+  if (chunk >= chunks.begin[a.n_workers]) return;
+  const int m = worker_of_block(chunks, a.n_workers, chunk);
+  const Chunk c = chunk_at(a, rows, chunks, m, chunk);
+  const uint32_t tok = lane < c.n ? a.tok[c.begin + lane] : 0;
+  const int col0 = blockIdx.y * kSlab + lane * VEC, cols = a.cols;
+  const TD* dy = static_cast<const TD*>(a.dy);
+  TG* table = static_cast<TG*>(grad.p[m]);
+  float* part = a.part + (int64_t)chunk * 2 * cols;
+  float acc[kLaneCols] = {};
+  bool first = true;
+  auto write_part = [&](int which) {
+#pragma unroll
+    for (int i = 0; i < kLaneCols; ++i) {
+      const int col = col0 + i / VEC * 32 * VEC + i % VEC;
+      if (col < cols) part[which * cols + col] = acc[i];
+    }
+  };
+  for (int j0 = 0; j0 < c.n; j0 += kBatch) {
+    typename RawVec<TD, VEC>::type raw[kBatch][kVecs];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint32_t row = __shfl_sync(0xffffffffu, tok, min(j0 + j, 31));
+      const TD* p = dy + (int64_t)row * a.ld_dy;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int col = col0 + i * 32 * VEC;
+        if (j0 + j < c.n && col < cols) raw[j][i] = load_stream<TD, VEC>(p + col);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint32_t key = __shfl_sync(0xffffffffu, c.key, min(j0 + j, 31));
+      if (j0 + j < c.n) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+          if (col0 + i * 32 * VEC < cols) {
+            float v[VEC];
+            unpack(raw[j][i], v);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[i * VEC + q] += v[q];
+          }
+        if (c.ends >> (j0 + j) & 1) {
+          if (first && c.from_before) write_part(0);
+          else write_grad<TG, VEC>(table + (int64_t)key * cols, col0, cols, a.accumulate, a.scale, acc);
+          first = false;
+#pragma unroll
+          for (int i = 0; i < kLaneCols; ++i) acc[i] = 0.f;
+        }
+      }
+    }
+  }
+  if (c.into_next) write_part(first && c.from_before ? 0 : 1);
+}
+
+// ------------------------------------------------------------------- join
+template <typename TG, int VEC>
+__global__ void __launch_bounds__(kJoinChunks * 32)
+join_kernel(const ReduceArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks chunks,
+            const __grid_constant__ WorkerPtrs grad) {
+  __shared__ int s_follow[kJoinChunks];
+  __shared__ uint32_t s_key[kJoinChunks];
+  __shared__ int s_worker[kJoinChunks];
+  __shared__ float s_acc[kJoinChunks][kSlab];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, cols = a.cols;
+  const int chunk0 = blockIdx.x * kJoinChunks, chunk = chunk0 + warp;
+  const int col0 = blockIdx.y * kSlab + lane * VEC;
+  int follow = 0, m = 0;
+  uint32_t key = 0;
+  if (chunk < chunks.begin[a.n_workers]) {
+    m = worker_of_block(chunks, a.n_workers, chunk);
+    const Chunk c = chunk_at(a, rows, chunks, m, chunk);
+    key = __shfl_sync(0xffffffffu, c.key, 31);
+    // A run that begins here (this chunk is not all one run from before) and
+    // goes on: how many chunks it goes on in.
+    if (c.into_next && (c.ends || !c.from_before)) {
+      int64_t lo = c.begin + kChunk + 1, hi = rows.begin[m + 1];
+      while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (a.key[mid] <= key) lo = mid + 1;
+        else hi = mid;
+      }
+      follow = (int)((lo - (c.begin + kChunk) + kChunk - 1) / kChunk);
+    }
+  }
+  // Adds the partial rows of chunk + i for i = from, from + step, ... <= n.
+  auto add = [&](int at, int from, int step, int n, float (&acc)[kLaneCols]) {
+#pragma unroll 4
+    for (int i = from; i <= n; i += step) {
+      const float* p = a.part + ((int64_t)(at + i) * 2 + (i == 0 ? 1 : 0)) * cols;
+#pragma unroll
+      for (int q = 0; q < kLaneCols; ++q) {
+        const int col = col0 + q / VEC * 32 * VEC + q % VEC;
+        if (col < cols) acc[q] += p[col];
+      }
+    }
+  };
+  const bool is_long = follow >= kLongRun;
+  if (lane == 0) s_follow[warp] = is_long ? follow : 0, s_key[warp] = key, s_worker[warp] = m;
+  if (follow && !is_long) {
+    float acc[kLaneCols] = {};
+    add(chunk, 0, 1, follow, acc);
+    write_grad<TG, VEC>(static_cast<TG*>(grad.p[m]) + (int64_t)key * cols, col0, cols, a.accumulate, a.scale, acc);
+  }
+  __syncthreads();
+  for (int w = 0; w < kJoinChunks; ++w) {
+    if (!s_follow[w]) continue;
+    float acc[kLaneCols] = {};
+    add(chunk0 + w, warp, kJoinChunks, s_follow[w], acc);
+#pragma unroll
+    for (int q = 0; q < kLaneCols; ++q) s_acc[warp][q * 32 + lane] = acc[q];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int q = 0; q < kLaneCols; ++q) {
+        acc[q] = 0.f;
+        for (int i = 0; i < kJoinChunks; ++i) acc[q] += s_acc[i][q * 32 + lane];
+      }
+      write_grad<TG, VEC>(static_cast<TG*>(grad.p[s_worker[w]]) + (int64_t)s_key[w] * cols, col0, cols, a.accumulate,
+                          a.scale, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------- host
+struct BackwardLayout {
+  size_t key[2], tok[2], part, total;
+};
+int64_t chunks_of(const int64_t* row_begin, int n_workers) {
+  int64_t n = 0;
+  for (int m = 0; m < n_workers; ++m) n += ceil_div(row_begin[m + 1] - row_begin[m], kChunk);
+  return n;
+}
+BackwardLayout backward_layout(int32_t cols, int n_workers, const int64_t* row_begin) {
+  const size_t n = round_up((size_t)row_begin[n_workers] * 4, 256);
+  BackwardLayout l;
+  l.key[0] = kWsHeaderBytes;
+  l.key[1] = l.key[0] + n;
+  l.tok[0] = l.key[1] + n;
+  l.tok[1] = l.tok[0] + n;
+  l.part = l.tok[1] + n;
+  l.total = l.part + round_up((size_t)chunks_of(row_begin, n_workers) * 2 * cols * 4, 256);
+  return l;
+}
+
+// Blocks of `per` rows for each worker.
+WorkerBlocks blocks_of(const int64_t* row_begin, int n_workers, int64_t per) {
+  WorkerBlocks b = {};
+  for (int m = 0; m < n_workers; ++m) b.begin[m + 1] = b.begin[m] + (int32_t)ceil_div(row_begin[m + 1] - row_begin[m], per);
+  return b;
+}
+
+template <int VEC>
+using Width = std::integral_constant<int, VEC>;
+
+// f(first type, second type, width) for a width that both types have.
+template <typename F>
+void by_types(signmuon_dtype a, signmuon_dtype b, int vec, F f) {
+  using bf16 = __nv_bfloat16;
+  if (a == SIGNMUON_F32 && b == SIGNMUON_F32) vec == 4 ? f(float(), float(), Width<4>()) : f(float(), float(), Width<1>());
+  else if (a == SIGNMUON_F32) vec == 4 ? f(float(), bf16(), Width<4>()) : f(float(), bf16(), Width<1>());
+  else if (b == SIGNMUON_F32) vec == 4 ? f(bf16(), float(), Width<4>()) : f(bf16(), float(), Width<1>());
+  else if (vec == 8) f(bf16(), bf16(), Width<8>());
+  else if (vec == 2) f(bf16(), bf16(), Width<2>());
+  else f(bf16(), bf16(), Width<1>());
+}
+// The widest access that both buffers allow.
+int common_width(signmuon_dtype ta, const void* a, int64_t lda, signmuon_dtype tb, const void* b, int64_t ldb, int32_t cols) {
+  if (ta == tb) return vec_narrow(vec_narrow(vec_width(ta, cols), ta, a, lda), tb, b, ldb);
+  const bool four = cols % 4 == 0 && lda % 4 == 0 && ldb % 4 == 0 && aligned_to(a, 4 * dtype_bytes(ta)) &&
+                    aligned_to(b, 4 * dtype_bytes(tb));
+  return four ? 4 : 1;
+}
+
+}  // namespace
+
+extern "C" {
+
+signmuon_status signmuon_embedding_forward(signmuon_shape table_shape, signmuon_dtype table_dtype, const void* table,
+                                           int64_t ld_table, int64_t n_tokens, int ids_int64, const void* ids,
+                                           float scale, signmuon_dtype y_dtype, void* y, int64_t ld_y, void* stream) {
+  const int32_t cols = table_shape.cols;
+  if (cols > kMaxCols) return SIGNMUON_ERR_UNSUPPORTED;
+  if (table_shape.rows <= 0 || cols <= 0 || n_tokens < 0 || !known_dtype(table_dtype) || !known_dtype(y_dtype) || !table ||
+      ld_table < cols || ld_y < cols || (n_tokens > 0 && (!ids || !y)))
+    return SIGNMUON_ERR_INVALID_ARG;
+  if (!aligned_to(table, dtype_bytes(table_dtype)) || !aligned_to(y, dtype_bytes(y_dtype)) || !aligned_to(ids, ids_int64 ? 8 : 4))
+    return SIGNMUON_ERR_ALIGNMENT;
+  const int vec = common_width(table_dtype, table, ld_table, y_dtype, y, ld_y, cols);
+  int lanes = 1;
+  while (lanes < 32 && lanes * vec < cols) lanes *= 2;
+  const int64_t blocks = ceil_div(n_tokens, kLookupThreads / lanes);
+  const int segments = (int)ceil_div(cols, (int64_t)lanes * vec * kLookupVecs);
+  if (blocks > INT32_MAX) return SIGNMUON_ERR_UNSUPPORTED;
+  if (!n_tokens) return SIGNMUON_OK;
+  by_types(table_dtype, y_dtype, vec, [&](auto tw, auto ty, auto v) {
+    lookup_kernel<decltype(tw), decltype(ty), decltype(v)::value>
+        <<<dim3((unsigned)blocks, (unsigned)segments), kLookupThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+            static_cast<const decltype(tw)*>(table), ld_table, table_shape.rows, cols, n_tokens, ids, ids_int64 != 0, scale,
+            static_cast<decltype(ty)*>(y), ld_y, lanes);
+  });
+  return cuda_status(cudaGetLastError());
+}
+
+static bool valid_backward_shape(signmuon_shape s, int n_workers, const int64_t* row_begin) {
+  return s.rows > 0 && s.cols > 0 && n_workers > 0 && n_workers <= SIGNMUON_MAX_WORKERS && row_begin &&
+         valid_splits(row_begin, n_workers, row_begin[n_workers]);
+}
+
+size_t signmuon_embedding_backward_workspace_bytes(signmuon_shape table_shape, int n_workers, const int64_t* row_begin) {
+  if (!valid_backward_shape(table_shape, n_workers, row_begin) || row_begin[n_workers] > INT32_MAX) return 0;
+  return backward_layout(table_shape.cols, n_workers, row_begin).total;
+}
+
+signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_workers, const int64_t* row_begin,
+                                            int ids_int64, const void* ids, signmuon_dtype dy_dtype, const void* dy,
+                                            int64_t ld_dy, float scale, int accumulate, signmuon_dtype grad_dtype,
+                                            void* const* grad, void* workspace, size_t ws_bytes, void* stream) {
+  const int32_t cols = table_shape.cols;
+  if (!valid_backward_shape(table_shape, n_workers, row_begin) || !known_dtype(dy_dtype) || !known_dtype(grad_dtype) ||
+      !grad || ld_dy < cols)
+    return SIGNMUON_ERR_INVALID_ARG;
+  const int64_t n = row_begin[n_workers];
+  if (cols > kMaxCols || n > INT32_MAX) return SIGNMUON_ERR_UNSUPPORTED;
+  if (n > 0 && (!ids || !dy)) return SIGNMUON_ERR_INVALID_ARG;
+  if (!aligned_to(ids, ids_int64 ? 8 : 4) || !aligned_to(dy, dtype_bytes(dy_dtype))) return SIGNMUON_ERR_ALIGNMENT;
+  Fill fill = {};
+  int vec = 8;
+  for (int m = 0; m < n_workers; ++m) {
+    if (!grad[m]) return SIGNMUON_ERR_INVALID_ARG;
+    if (!aligned_to(grad[m], dtype_bytes(grad_dtype))) return SIGNMUON_ERR_ALIGNMENT;
+    fill.grad.p[m] = grad[m];
+    const int v = common_width(dy_dtype, dy, ld_dy, grad_dtype, grad[m], cols, cols);
+    if (v < vec) vec = v;
+  }
+  const BackwardLayout l = backward_layout(cols, n_workers, row_begin);
+  const signmuon_status st = check_ws(workspace, ws_bytes, l.total);
+  if (st) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint32_t* key[2] = {reinterpret_cast<uint32_t*>(ws + l.key[0]), reinterpret_cast<uint32_t*>(ws + l.key[1])};
+  uint32_t* tok[2] = {reinterpret_cast<uint32_t*>(ws + l.tok[0]), reinterpret_cast<uint32_t*>(ws + l.tok[1])};
+  WorkerRows rows = {};
+  int64_t longest = 0;
+  for (int m = 0; m <= n_workers; ++m) {
+    rows.begin[m] = row_begin[m];
+    if (m && row_begin[m] - row_begin[m - 1] > longest) longest = row_begin[m] - row_begin[m - 1];
+  }
+
+  // Sort (keys 0 .. rows) and fill.
+  int key_bits = 1;
+  while (key_bits < 31 && (table_shape.rows >> key_bits)) ++key_bits;
+  const int passes = (key_bits + kDigitBits - 1) / kDigitBits, bits = (key_bits + passes - 1) / passes;
+  const WorkerBlocks tiles = blocks_of(row_begin, n_workers, kTile);
+  fill.bytes = accumulate ? 0 : (int64_t)table_shape.rows * cols * dtype_bytes(grad_dtype);
+  int64_t fill_blocks = accumulate ? 0 : ceil_div(fill.bytes * n_workers, 65536);
+  if (fill_blocks > 2 * current_sms()) fill_blocks = 2 * current_sms();
+  const int64_t grid = tiles.begin[n_workers] + fill_blocks;
+  if (!grid) return SIGNMUON_OK;
+  constexpr int kCountBytes = kSortWarps * kDigits * 2;
+  cudaError_t e = cudaFuncSetAttribute(sort_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCountBytes);
+  if (e != cudaSuccess) return cuda_status(e);
+  sort_tiles_kernel<<<(unsigned)grid, kSortThreads, kCountBytes, cs>>>(rows, tiles, n_workers, ids, ids_int64 != 0,
+                                                                      (uint32_t)table_shape.rows, passes, bits, key[0], tok[0],
+                                                                      fill);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
+  if (!n) return SIGNMUON_OK;
+
+  int at = 0;
+  for (int64_t run = kTile; run < longest; run *= kFan, at ^= 1) {
+    const WorkerBlocks blocks = blocks_of(row_begin, n_workers, kMergeThreads);
+    merge_kernel<<<blocks.begin[n_workers], kMergeThreads, 0, cs>>>(rows, blocks, n_workers, run, key[at], tok[at],
+                                                                    key[at ^ 1], tok[at ^ 1]);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
+  }
+
+  const WorkerBlocks chunks = blocks_of(row_begin, n_workers, kChunk);
+  const int n_chunks = chunks.begin[n_workers];
+  ReduceArgs a = {};
+  a.key = key[at], a.tok = tok[at], a.dy = dy, a.ld_dy = ld_dy, a.part = reinterpret_cast<float*>(ws + l.part);
+  a.vocab = (uint32_t)table_shape.rows, a.cols = cols, a.n_workers = n_workers, a.accumulate = accumulate != 0, a.scale = scale;
+  const unsigned slabs = (unsigned)ceil_div(cols, kSlab);
+  by_types(dy_dtype, grad_dtype, vec, [&](auto td, auto tg, auto v) {
+    reduce_kernel<decltype(td), decltype(tg), decltype(v)::value>
+        <<<dim3((unsigned)ceil_div(n_chunks, kReduceThreads / 32), slabs), kReduceThreads, 0, cs>>>(a, rows, chunks, fill.grad);
+    if ((e = cudaGetLastError()) != cudaSuccess) return;
+    join_kernel<decltype(tg), decltype(v)::value>
+        <<<dim3((unsigned)ceil_div(n_chunks, kJoinChunks), slabs), kJoinChunks * 32, 0, cs>>>(a, rows, chunks, fill.grad);
+    e = cudaGetLastError();
+  });
+  return cuda_status(e);
+}
+
+}  // extern "C"
