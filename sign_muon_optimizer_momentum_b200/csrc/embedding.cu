@@ -192,36 +192,47 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
 
 // ------------------------------------------------------------------ merge
 // Runs of `run` sorted pairs of each worker, kFan at a time, to runs of
-// kFan * run.  Equal keys keep the runs' order.
+// kFan * run (run is a power of two).  Equal keys keep the runs' order.
 __global__ void __launch_bounds__(kMergeThreads)
-merge_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks blocks, int n_workers, int64_t run,
+merge_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks blocks, int n_workers, int run,
              const uint32_t* __restrict__ key, const uint32_t* __restrict__ tok, uint32_t* __restrict__ out_key,
              uint32_t* __restrict__ out_tok) {
   const int m = worker_of_block(blocks, n_workers, blockIdx.x);
-  const int64_t n = rows.begin[m + 1] - rows.begin[m];
-  const int64_t p = (int64_t)(blockIdx.x - blocks.begin[m]) * kMergeThreads + threadIdx.x;
+  const int n = (int)(rows.begin[m + 1] - rows.begin[m]);  // at most 2^31 - 1 tokens in all
+  const int p = (blockIdx.x - blocks.begin[m]) * kMergeThreads + threadIdx.x;
   if (p >= n) return;
   key += rows.begin[m];
   const uint32_t k = key[p];
-  const int64_t mine = p / run, group = mine / kFan * kFan;
-  int64_t place = group * run + (p - mine * run);
-#pragma unroll 4
-  for (int i = 0; i < kFan; ++i) {
-    const int64_t other = group + i, begin = other * run;
-    if (other == mine || begin >= n) continue;
-    // Pairs of the other run that go before: keys below k, and equal ones of
-    // an earlier run.
-    const uint32_t below = k + (other < mine ? 1u : 0u);
-    int64_t lo = begin, hi = min(begin + run, n);
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (key[mid] < below) lo = mid + 1;
-      else hi = mid;
+  const int mine = p / run, group = mine / kFan * kFan, own = mine - group;
+  const int runs = min(kFan, (n + run - 1) / run - group);
+  // Pairs of the other runs that go before: keys below k, and equal ones of
+  // an earlier run.  kBatch searches go side by side, without branches: one
+  // alone would wait for each of its loads.
+  constexpr int kBatch = 8;
+  int before = 0;
+  for (int i0 = 0; i0 < runs; i0 += kBatch) {
+    int at[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) at[i] = 0;
+    for (int step = run; step; step /= 2) {
+      uint32_t seen[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int begin = (group + min(i0 + i, runs - 1)) * run;
+        seen[i] = key[begin + min(at[i] + step, min(run, n - begin)) - 1];
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int begin = (group + min(i0 + i, runs - 1)) * run, probe = at[i] + step;
+        at[i] = probe <= min(run, n - begin) && seen[i] < k + (i0 + i < own ? 1u : 0u) ? probe : at[i];
+      }
     }
-    place += lo - begin;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) before += i0 + i < runs && i0 + i != own ? at[i] : 0;
   }
-  out_key[rows.begin[m] + place] = k;
-  out_tok[rows.begin[m] + place] = tok[rows.begin[m] + p];
+  const int64_t place = rows.begin[m] + (int64_t)group * run + (p - mine * run) + before;
+  out_key[place] = k;
+  out_tok[place] = tok[rows.begin[m] + p];
 }
 
 // ----------------------------------------------------------------- reduce
@@ -547,18 +558,18 @@ signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_wo
   const int64_t grid = tiles.begin[n_workers] + fill_blocks;
   if (!grid) return SIGNMUON_OK;
   constexpr int kCountBytes = kSortWarps * kDigits * 2;
-  cudaError_t e = cudaFuncSetAttribute(sort_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCountBytes);
-  if (e != cudaSuccess) return cuda_status(e);
+  resident_blocks<sort_tiles_kernel>(kSortThreads, kCountBytes);  // allows it the shared memory
   sort_tiles_kernel<<<(unsigned)grid, kSortThreads, kCountBytes, cs>>>(rows, tiles, n_workers, ids, ids_int64 != 0,
                                                                       (uint32_t)table_shape.rows, passes, bits, key[0], tok[0],
                                                                       fill);
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e);
   if (!n) return SIGNMUON_OK;
 
   int at = 0;
   for (int64_t run = kTile; run < longest; run *= kFan, at ^= 1) {
     const WorkerBlocks blocks = blocks_of(row_begin, n_workers, kMergeThreads);
-    merge_kernel<<<blocks.begin[n_workers], kMergeThreads, 0, cs>>>(rows, blocks, n_workers, run, key[at], tok[at],
+    merge_kernel<<<blocks.begin[n_workers], kMergeThreads, 0, cs>>>(rows, blocks, n_workers, (int)run, key[at], tok[at],
                                                                     key[at ^ 1], tok[at ^ 1]);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
   }

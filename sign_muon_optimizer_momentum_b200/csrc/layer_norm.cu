@@ -11,7 +11,9 @@
 // x and dy and writes dx, each once.  A row is held in the registers of the
 // group of threads that works on it (kE elements a thread), so both of the
 // variance's passes and the backward's two sums cost no second read; groups
-// walk over rows with the next row's loads in flight.  The backward adds dy xh
+// walk over rows, and each thread keeps its part of the next rows coming by
+// asynchronous copies into a ring of its own in shared memory (no barrier:
+// a thread reads back only what it copied).  The backward adds dy xh
 // and dy of its rows to per-thread column sums, adds those of a block's groups
 // in shared memory, and leaves one row of partial sums a block; a second
 // launch adds a worker's blocks.  All sums have a fixed order.
@@ -21,15 +23,16 @@ using namespace signmuon;
 
 namespace {
 
-constexpr int kMaxThreads = 1024;     // forward: threads a block at most
-constexpr int kBwdThreads = 512;      // backward: its column sums need up to 128 registers a thread
-constexpr int kGroupThreads = 256;    // threads a block where a row needs fewer
-constexpr int kWideThreads = 512;     // rows too long for registers
+constexpr int kWarpCols = 1024;       // longest row that one warp takes (32 elements a lane)
+constexpr int kThreads = 256;         // threads a block where a warp or less takes a row
+constexpr int kBlockElems = 16;       // elements a thread where a block takes a row
+constexpr int kBlockThreads = 512;    // threads of such a block at most (8192 columns)
+constexpr int kWideThreads = 512;     // rows longer still
 
 // Rows and columns of one call.
 struct NormArgs {
   int64_t rows;
-  int32_t cols, tpr;                  // threads a row (a multiple of 32)
+  int32_t cols;
   const void* x;
   const void* dy;
   void* out;                          // y or dx
@@ -43,124 +46,209 @@ struct NormArgs {
   float* part;                        // backward: [blocks][sums][cols]
   int32_t n_workers, has_bias;
 };
-// Barrier of one group of a block (1 .. 8; 0 is __syncthreads').
-__device__ __forceinline__ void group_sync(int group, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
-}
-
-template <typename T, int VEC, int E>
-struct Row {
+// A thread's part of a row: chunk c is the VEC elements from column
+// (c * tpr + t) * VEC, tpr threads to a row.  Rows come through kSlots slots
+// of shared memory; single bf16 (2 bytes, below what can be copied
+// asynchronously) are loaded when they are needed.
+template <typename T, int VEC, int E, int kSlots>
+struct Rows {
+  using Raw = typename RawVec<T, VEC>::type;
   static constexpr int kChunks = E / VEC;
-  typename RawVec<T, VEC>::type raw[kChunks];
-  __device__ __forceinline__ void load(const T* p, int t, int tpr, int cols) {
+  static constexpr bool kAsync = sizeof(Raw) >= 4;
+  static constexpr size_t bytes(int threads) { return kAsync ? (size_t)kSlots * kChunks * sizeof(Raw) * threads : 0; }
+  Raw* ring;
+  int t, tpr, cols;
+  // Slots past the last column are 0 from the start and stay so.
+  __device__ __forceinline__ Rows(void* smem, int t, int tpr, int cols)
+      : ring(static_cast<Raw*>(smem) + threadIdx.x), t(t), tpr(tpr), cols(cols) {
+    if constexpr (kAsync) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int col = (c * tpr + t) * VEC;
-      if (col < cols) raw[c] = load_stream<T, VEC>(p + col);
+      for (int c = 0; c < kChunks; ++c)
+        if ((c * tpr + t) * VEC >= cols)
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i) ring[(i * kChunks + c) * blockDim.x] = Raw{};
+    }
+  }
+  __device__ __forceinline__ void fetch(const T* p, int slot) const {
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int col = (c * tpr + t) * VEC;
+        if (col < cols) copy_async<sizeof(Raw)>(ring + (slot * kChunks + c) * blockDim.x, p + col);
+      }
     }
   }
   // Elements past the last column are 0.
-  __device__ __forceinline__ void get(float (&v)[E], int t, int tpr, int cols) const {
+  __device__ __forceinline__ void get(float (&v)[E], const T* p, int slot) const {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       float u[VEC];
-      unpack(raw[c], u);
-      const bool in = (c * tpr + t) * VEC < cols;
+      if constexpr (kAsync) {
+        unpack(ring[(slot * kChunks + c) * blockDim.x], u);
+      } else {
+        const int col = (c * tpr + t) * VEC;
+        u[0] = 0.f;
+        if (col < cols) unpack(load_stream<T, VEC>(p + col), u);
+      }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[c * VEC + j] = in ? u[j] : 0.f;
+      for (int j = 0; j < VEC; ++j) v[c * VEC + j] = u[j];
     }
   }
 };
+// Slots of a ring: about 192 bytes of rows a thread, two rows at least.
+template <typename T, int E>
+constexpr int kRowSlots = 192 / (E * (int)sizeof(T)) < 2 ? 2 : 192 / (E * (int)sizeof(T)) > 4 ? 4 : 192 / (E * (int)sizeof(T));
 
-template <int VEC, int E>
-__device__ __forceinline__ void load_weights(const void* w, int bf16, int t, int tpr, int cols, float (&v)[E]) {
+// A thread's weights (zero past the last column).  Where a block takes a row:
+// in registers, as they are stored (W is the type).  Where a warp or less
+// takes a row, a thread has too many for that: fp32 in shared memory, each
+// group of four of the kTpr lanes side by side, so that reads meet no bank
+// conflict (rows of eight by lane cost twice the reads, which then bound the
+// forward kernel).
+template <typename W, int VEC, int E>
+struct RegWeights {
+  static constexpr bool kBf16 = sizeof(W) == 2;
+  uint32_t reg[kBf16 ? E / 2 : E];
+  __device__ __forceinline__ void load(const void* w, int, float*, int t, int tpr, int cols) {
+    uint32_t v[E];
 #pragma unroll
-  for (int c = 0; c < E / VEC; ++c)
+    for (int i = 0; i < E; ++i) {
+      const int col = (i / VEC * tpr + t) * VEC + i % VEC;
+      v[i] = w && col < cols ? __float_as_uint(load_elem(w, col, kBf16)) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < (kBf16 ? E / 2 : E); ++i) reg[i] = kBf16 ? v[2 * i % E] >> 16 | v[(2 * i + 1) % E] : v[i];
+  }
+  __device__ __forceinline__ void get(int c, float (&v)[VEC]) const {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const int col = (c * tpr + t) * VEC + j;
-      v[c * VEC + j] = col < cols ? load_elem(w, col, bf16) : 0.f;
+      const int i = c * VEC + j;
+      if constexpr (kBf16) v[j] = i % 2 ? bf16_hi(reg[i / 2]) : bf16_lo(reg[i / 2]);
+      else v[j] = __uint_as_float(reg[i]);
     }
+  }
+};
+template <int VEC, int E, int kTpr>
+struct SharedWeights {
+  const float* sh;  // this lane's first
+  __device__ __forceinline__ void load(const void* w, int bf16, float* smem, int t, int, int cols) {
+    // Element q of group g (of min(VEC, 4)) of chunk c of lane l.
+    for (int col = threadIdx.x; col < E * kTpr; col += kThreads) {
+      const int c = col / (kTpr * VEC), l = col / VEC % kTpr, j = col % VEC;
+      smem[at(c, j) + l * kGroup] = w && col < cols ? load_elem(w, col, bf16) : 0.f;
+    }
+    sh = smem + t * kGroup;
+  }
+  static constexpr int kGroup = VEC < 4 ? VEC : 4;
+  __device__ __forceinline__ static int at(int c, int j) { return (c * (VEC / kGroup) + j / kGroup) * kTpr * kGroup + j % kGroup; }
+  __device__ __forceinline__ void get(int c, float (&v)[VEC]) const {
+#pragma unroll
+    for (int j = 0; j < VEC; j += kGroup) {
+      if constexpr (kGroup == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(sh + at(c, j));
+        v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
+      } else if constexpr (kGroup == 2) {
+        const float2 q = *reinterpret_cast<const float2*>(sh + at(c, j));
+        v[j] = q.x, v[j + 1] = q.y;
+      } else {
+        v[j] = sh[at(c, j)];
+      }
+    }
+  }
+};
+template <typename W, int VEC, int E, int kTpr>
+using Weights = std::conditional_t<kTpr == 0, RegWeights<W, VEC, E>, SharedWeights<VEC, E, kTpr>>;
+
+// Sum over the kTpr lanes of a row's group (kTpr <= 32), or over the block
+// (kTpr == 0) by way of sh.  Blocks alternate between two arrays, so that one
+// barrier a sum does.
+template <int kTpr>
+__device__ __forceinline__ float row_sum(float v, float* sh) {
+#pragma unroll
+  for (int o = (kTpr ? kTpr : 32) / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (kTpr == 0) {
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    const float4* q = reinterpret_cast<const float4*>(sh);
+    v = 0.f;
+    for (int i = 0; i < (int)blockDim.x / 32; i += 4) {
+      const float4 p = q[i / 4];  // zero past the block's warps
+      v += (p.x + p.y) + (p.z + p.w);
+    }
+  }
+  return v;
 }
 
 // --------------------------------------------------------------- forward
-// The variance is centred: each warp takes its part's own mean and sum of
-// squares about it, and the parts are joined as
-//   M2 = sum M2_i + sum n_i (mu_i - mu)^2
-// so that one exchange through shared memory serves both passes.
-template <typename T, int VEC, int E>
-__global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormArgs a) {
-  __shared__ float2 sh[2][32];
-  __shared__ float sh_n[32];  // elements of a row that each warp of a group holds
-  const int tpr = a.tpr, t = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  const int lane = threadIdx.x & 31, warps = tpr / 32, w0 = group * warps, cols = a.cols;
-  float w[E], b[E];
-  load_weights<VEC, E>(a.w, a.w_bf16, t, tpr, cols, w);
-  if (a.b) load_weights<VEC, E>(a.b, a.w_bf16, t, tpr, cols, b);
-  else
-#pragma unroll
-    for (int i = 0; i < E; ++i) b[i] = 0.f;
-  float mine = 0.f;  // this thread's elements
-#pragma unroll
-  for (int c = 0; c < E / VEC; ++c) mine += (c * tpr + t) * VEC < cols ? (float)VEC : 0.f;
-  const float n_warp = warp_sum(mine), inv_cols = 1.f / (float)cols;
-  if (threadIdx.x < tpr && lane == 0) sh_n[threadIdx.x / 32] = n_warp;
-  __syncthreads();
+// kTpr lanes (8, 16 or 32) a row, or 0: a block a row.  The variance is taken
+// about the mean, from the values in registers.
+template <typename T, typename W, int VEC, int E, int kTpr>
+__global__ void __launch_bounds__(kTpr ? kThreads : kBlockThreads) norm_forward_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float sh[2][kBlockThreads / 32];
+  constexpr bool kBlock = kTpr == 0;
+  constexpr int kSlots = kRowSlots<T, E>;
+  const int tpr = kBlock ? blockDim.x : kTpr, t = threadIdx.x % tpr, cols = a.cols;
+  constexpr int groups = kBlock ? 1 : kThreads / (kBlock ? 1 : kTpr);
+  const float inv_cols = 1.f / (float)cols;
   const T* x = static_cast<const T*>(a.x);
   T* y = static_cast<T*>(a.out);
 
+  // All lanes of a warp run the same iterations (`first` is the row of the
+  // warp's first lane); rows past the end are masked.
   const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row = (int64_t)blockIdx.x * groups + group;
-  Row<T, VEC, E> cur, next;
-  if (row < a.rows) cur.load(x + row * a.ld_x, t, tpr, cols);
-  for (int it = 0; row < a.rows; row += step, it ^= 1) {
-    if (row + step < a.rows) next.load(x + (row + step) * a.ld_x, t, tpr, cols);
+  int64_t row = (int64_t)blockIdx.x * groups + threadIdx.x / tpr;
+  int64_t first = (int64_t)blockIdx.x * groups + threadIdx.x / 32 * 32 / tpr;
+  const Rows<T, VEC, E, kSlots> in(smem, t, tpr, cols);
+#pragma unroll
+  for (int i = 0; i < kSlots - 1; ++i) {
+    if (row + i * step < a.rows) in.fetch(x + (row + i * step) * a.ld_x, i);
+    copy_commit();
+  }
+  float* w_sh = reinterpret_cast<float*>(smem + Rows<T, VEC, E, kSlots>::bytes(blockDim.x));
+  Weights<W, VEC, E, kTpr> w, b;
+  w.load(a.w, a.w_bf16, w_sh, t, tpr, cols);
+  b.load(a.b, a.w_bf16, w_sh + E * kTpr, t, tpr, cols);
+  if (threadIdx.x < 2 * kBlockThreads / 32) sh[0][threadIdx.x] = 0.f;
+  __syncthreads();
+
+  int slot = 0;
+  for (; first < a.rows; row += step, first += step) {
+    const int64_t ahead = row + (kSlots - 1) * step;
+    if (ahead < a.rows) in.fetch(x + ahead * a.ld_x, slot == 0 ? kSlots - 1 : slot - 1);
+    copy_commit();
+    copy_wait<kSlots - 1>();
+    const bool valid = row < a.rows;
     float v[E];
-    cur.get(v, t, tpr, cols);
+    in.get(v, x + (valid ? row : 0) * a.ld_x, slot);
+    slot = slot == kSlots - 1 ? 0 : slot + 1;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) s += v[i];
-    s = warp_sum(s);
-    float mean = warps == 1 ? s * inv_cols : n_warp > 0.f ? s / n_warp : 0.f;
-    float m2 = 0.f;
+    const float mean = row_sum<kTpr>(s, sh[0]) * inv_cols;
+    s = 0.f;
 #pragma unroll
     for (int c = 0; c < E / VEC; ++c)
       if ((c * tpr + t) * VEC < cols)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float d = v[c * VEC + j] - mean;
-          m2 = fmaf(d, d, m2);
+          v[c * VEC + j] -= mean;
+          s = fmaf(v[c * VEC + j], v[c * VEC + j], s);
         }
-    m2 = warp_sum(m2);
-    if (warps > 1) {
-      if (lane == 0) sh[it][threadIdx.x / 32] = make_float2(s, m2);
-      group_sync(group, tpr);
-      float total = 0.f;
-      for (int i = 0; i < warps; ++i) total += sh[it][w0 + i].x;
-      mean = total * inv_cols;
-      m2 = 0.f;
-      for (int i = 0; i < warps; ++i) {
-        const float n = sh_n[i];
-        if (n > 0.f) {
-          const float2 p = sh[it][w0 + i];
-          const float d = __fdividef(p.x, n) - mean;
-          m2 += p.y + n * d * d;
-        }
-      }
-    }
-    const float r = rsqrtf(m2 * inv_cols + a.eps);
-    if (t == 0) a.mean[row] = mean, a.rstd[row] = r;
+    const float r = rsqrtf(row_sum<kTpr>(s, sh[1]) * inv_cols + a.eps);
+    if (t == 0 && valid) a.mean[row] = mean, a.rstd[row] = r;
 #pragma unroll
     for (int c = 0; c < E / VEC; ++c) {
       const int col = (c * tpr + t) * VEC;
-      if (col < cols) {
-        float o[VEC];
+      if (col < cols && valid) {
+        float o[VEC], wv[VEC], bv[VEC];
+        w.get(c, wv);
+        b.get(c, bv);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = fmaf((v[c * VEC + j] - mean) * r, w[c * VEC + j], b[c * VEC + j]);
+        for (int j = 0; j < VEC; ++j) o[j] = fmaf(v[c * VEC + j] * r, wv[j], bv[j]);
         store_stream<T, VEC>(y + row * a.ld_out + col, o);
       }
     }
-    cur = next;
   }
 }
 
@@ -210,99 +298,139 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const N
 }
 
 // -------------------------------------------------------------- backward
-template <typename T, int VEC, int E>
-__global__ void __launch_bounds__(kBwdThreads)
+template <typename T, typename W, int VEC, int E, int kTpr>
+__global__ void __launch_bounds__(kTpr ? kThreads : kBlockThreads)
 norm_backward_kernel(const NormArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks share) {
-  extern __shared__ float cols_sh[];  // [sums][cols] (blocks of more than one group)
-  __shared__ float2 sh[2][32];
-  const int tpr = a.tpr, t = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  const int lane = threadIdx.x & 31, warps = tpr / 32, w0 = group * warps, cols = a.cols;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float sh[2][2][kBlockThreads / 32];
+  constexpr bool kBlock = kTpr == 0;
+  constexpr int kSlots = kRowSlots<T, 2 * E>;
+  const int tpr = kBlock ? blockDim.x : kTpr, t = threadIdx.x % tpr, cols = a.cols;
+  constexpr int groups = kBlock ? 1 : kThreads / (kBlock ? 1 : kTpr);
   const int m = worker_of_block(share, a.n_workers, blockIdx.x);
   const int blocks = share.begin[m + 1] - share.begin[m];
-  float w[E], dw[E], db[E];
-  load_weights<VEC, E>(a.w, a.w_bf16, t, tpr, cols, w);
-#pragma unroll
-  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.f;
   const float inv_cols = 1.f / (float)cols;
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
   T* dx = static_cast<T*>(a.out);
 
   const int64_t step = (int64_t)blocks * groups, end = rows.begin[m + 1];
-  int64_t row = rows.begin[m] + (int64_t)(blockIdx.x - share.begin[m]) * groups + group;
-  Row<T, VEC, E> cx, cg, nx, ng;
-  float mean = 0.f, r = 0.f, mean_next = 0.f, r_next = 0.f;
-  if (row < end) {
-    cx.load(x + row * a.ld_x, t, tpr, cols);
-    cg.load(dy + row * a.ld_dy, t, tpr, cols);
-    mean = a.mean[row], r = a.rstd[row];
-  }
-  for (int it = 0; row < end; row += step, it ^= 1) {
-    if (row + step < end) {
-      nx.load(x + (row + step) * a.ld_x, t, tpr, cols);
-      ng.load(dy + (row + step) * a.ld_dy, t, tpr, cols);
-      mean_next = a.mean[row + step], r_next = a.rstd[row + step];
-    }
-    float xh[E], g[E], s1 = 0.f, s2 = 0.f;
-    cx.get(xh, t, tpr, cols);
-    cg.get(g, t, tpr, cols);
+  int64_t first = rows.begin[m] + (int64_t)(blockIdx.x - share.begin[m]) * groups;
+  int64_t row = first + threadIdx.x / tpr;
+  first += threadIdx.x / 32 * 32 / tpr;
+  using Ring = Rows<T, VEC, E, kSlots>;
+  const Ring in_x(smem, t, tpr, cols), in_g(smem + Ring::bytes(blockDim.x), t, tpr, cols);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      xh[i] = (xh[i] - mean) * r;  // past the last column g is 0, so this drops out
-      db[i] += g[i];
-      dw[i] += (i / VEC * tpr + t) * VEC < cols ? g[i] * xh[i] : 0.f;
-      g[i] *= w[i];
-      s1 += g[i];
-      s2 += (i / VEC * tpr + t) * VEC < cols ? g[i] * xh[i] : 0.f;
+  for (int i = 0; i < kSlots - 1; ++i) {
+    if (row + i * step < end) in_x.fetch(x + (row + i * step) * a.ld_x, i), in_g.fetch(dy + (row + i * step) * a.ld_dy, i);
+    copy_commit();
+  }
+  float mean_next = 0.f, r_next = 0.f;
+  if (row < end) mean_next = a.mean[row], r_next = a.rstd[row];
+  Weights<W, VEC, E, kTpr> w;
+  w.load(a.w, a.w_bf16, reinterpret_cast<float*>(smem + 2 * Ring::bytes(blockDim.x)), t, tpr, cols);
+  if (threadIdx.x < 4 * kBlockThreads / 32) sh[0][0][threadIdx.x] = 0.f;
+  __syncthreads();
+
+  float dw[E], db[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.f;
+  int slot = 0;
+  for (int it = 0; first < end; row += step, first += step, it ^= 1) {
+    const int64_t ahead = row + (kSlots - 1) * step;
+    if (ahead < end) {
+      const int to = slot == 0 ? kSlots - 1 : slot - 1;
+      in_x.fetch(x + ahead * a.ld_x, to), in_g.fetch(dy + ahead * a.ld_dy, to);
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (warps > 1) {
-      if (lane == 0) sh[it][threadIdx.x / 32] = make_float2(s1, s2);
-      group_sync(group, tpr);
-      s1 = s2 = 0.f;
-      for (int i = 0; i < warps; ++i) {
-        const float2 p = sh[it][w0 + i];
-        s1 += p.x;
-        s2 += p.y;
-      }
-    }
-    s1 *= inv_cols;
-    s2 *= inv_cols;
+    copy_commit();
+    const float mean = mean_next, r = r_next;
+    if (row + step < end) mean_next = a.mean[row + step], r_next = a.rstd[row + step];
+    copy_wait<kSlots - 1>();
+    const bool valid = row < end;
+    float xh[E], g[E], s1 = 0.f, s2 = 0.f;
+    in_x.get(xh, x + (valid ? row : 0) * a.ld_x, slot);
+    in_g.get(g, dy + (valid ? row : 0) * a.ld_dy, slot);
+    slot = slot == kSlots - 1 ? 0 : slot + 1;
 #pragma unroll
     for (int c = 0; c < E / VEC; ++c) {
       const int col = (c * tpr + t) * VEC;
-      if (col < cols) {
+      if (col < cols && valid) {
+        float wv[VEC];
+        w.get(c, wv);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const int i = c * VEC + j;
+          xh[i] = (xh[i] - mean) * r;
+          db[i] += g[i];
+          dw[i] = fmaf(g[i], xh[i], dw[i]);
+          g[i] *= wv[j];
+          s1 += g[i];
+          s2 = fmaf(g[i], xh[i], s2);
+        }
+      }
+    }
+    if constexpr (kBlock) {
+      // Both sums with one barrier; the arrays alternate by rows.
+      s1 = warp_sum(s1);
+      s2 = warp_sum(s2);
+      if ((threadIdx.x & 31) == 0) sh[it][0][threadIdx.x / 32] = s1, sh[it][1][threadIdx.x / 32] = s2;
+      __syncthreads();
+      s1 = s2 = 0.f;
+      for (int i = 0; i < (int)blockDim.x / 32; i += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(&sh[it][0][i]), q = *reinterpret_cast<const float4*>(&sh[it][1][i]);
+        s1 += (p.x + p.y) + (p.z + p.w);
+        s2 += (q.x + q.y) + (q.z + q.w);
+      }
+    } else {
+      s1 = row_sum<kTpr>(s1, nullptr);
+      s2 = row_sum<kTpr>(s2, nullptr);
+    }
+    const float c1 = -r * s1 * inv_cols, c2 = -r * s2 * inv_cols;
+#pragma unroll
+    for (int c = 0; c < E / VEC; ++c) {
+      const int col = (c * tpr + t) * VEC;
+      if (col < cols && valid) {
         float o[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = r * (g[c * VEC + j] - s1 - xh[c * VEC + j] * s2);
+        for (int j = 0; j < VEC; ++j) o[j] = fmaf(xh[c * VEC + j], c2, fmaf(g[c * VEC + j], r, c1));
         store_stream<T, VEC>(dx + row * a.ld_out + col, o);
       }
     }
-    cx = nx, cg = ng, mean = mean_next, r = r_next;
   }
 
-  // The block's partial sums: its groups one after another.
+  // The block's partial sums.
   const int sums = a.has_bias ? 2 : 1;
   float* part = a.part + (int64_t)blockIdx.x * sums * cols;
-  float* acc = groups > 1 ? cols_sh : part;
-  for (int g = 0; g < groups; ++g) {
-    if (g) __syncthreads();
-    if (g == group)
+  if constexpr (kBlock) {
 #pragma unroll
-      for (int c = 0; c < E / VEC; ++c)
+    for (int i = 0; i < E; ++i) {
+      const int col = (i / VEC * tpr + t) * VEC + i % VEC;
+      if (col < cols) {
+        part[col] = dw[i];
+        if (a.has_bias) part[cols + col] = db[i];
+      }
+    }
+  } else {
+    // Every group's in shared memory (over the rings and weights), then added
+    // by column in the groups' order; one sum after the other, which bounds
+    // the room at 4 kThreads E bytes.
+    float* all = reinterpret_cast<float*>(smem);
+    constexpr int kCols = kTpr * E;
+    for (int q = 0; q < sums; ++q) {
+      __syncthreads();
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int col = (c * tpr + t) * VEC + j;
-          if (col < cols) {
-            acc[col] = (g ? acc[col] : 0.f) + dw[c * VEC + j];
-            if (a.has_bias) acc[cols + col] = (g ? acc[cols + col] : 0.f) + db[c * VEC + j];
-          }
-        }
-  }
-  if (groups > 1) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < sums * cols; i += blockDim.x) part[i] = cols_sh[i];
+      for (int i = 0; i < E; ++i) {
+        const int col = (i / VEC * kTpr + t) * VEC + i % VEC;
+        all[threadIdx.x / kTpr * kCols + col] = q ? db[i] : dw[i];
+      }
+      __syncthreads();
+      for (int col = threadIdx.x; col < cols; col += kThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int g = 0; g < groups; ++g) s += all[g * kCols + col];
+        part[q * cols + col] = s;
+      }
+    }
   }
 }
 
@@ -393,35 +521,49 @@ norm_finalize_kernel(const float* part, int cols, int sums, int w_bf16, const __
 }
 
 // ------------------------------------------------------------------ host
-// Elements a thread holds and threads a row for rows of `cols` elements:
-// 8 elements up to `threads` x 8 columns, else 16; 0 where a block's threads
-// cannot hold the row.
-struct RowShape {
-  int e, tpr;
-};
-RowShape row_shape(int cols, int threads, int vec) {
-  RowShape s;
-  s.e = cols <= 8 * kGroupThreads ? 8 : 16;
-  if (s.e < vec) s.e = vec;
-  s.tpr = (cols + 32 * s.e - 1) / (32 * s.e) * 32;
-  if (s.tpr > threads) s.e = 0;
-  return s;
+template <int N>
+using Int = std::integral_constant<int, N>;
+// f(elements a lane, lanes a row) for the kernels where a warp or less takes
+// a row: as few lanes as hold it with 8 elements each, then more elements.
+template <typename F>
+void by_lanes(int cols, F f) {
+  if (cols <= 64) f(Int<8>(), Int<8>());
+  else if (cols <= 128) f(Int<8>(), Int<16>());
+  else if (cols <= 256) f(Int<8>(), Int<32>());
+  else if (cols <= 512) f(Int<16>(), Int<32>());
+  else if (cols <= 768) f(Int<24>(), Int<32>());
+  else f(Int<32>(), Int<32>());
 }
-int groups_of(int tpr) { return tpr >= kGroupThreads ? 1 : kGroupThreads / tpr; }
+template <typename F>
+void by_weight(int bf16, F f) {
+  if (bf16) f(__nv_bfloat16());
+  else f(float());
+}
+int block_threads(int cols) { return (int)round_up((size_t)ceil_div(cols, kBlockElems), 32); }
 
 template <typename T, int VEC>
-void forward_launch(const NormArgs& a, RowShape s, int sms, cudaStream_t st) {
-  if (!s.e) {
-    const int64_t grid = a.rows < (int64_t)sms * 4 ? a.rows : (int64_t)sms * 4;
-    norm_forward_wide_kernel<T, VEC><<<(unsigned)grid, kWideThreads, 0, st>>>(a);
-    return;
+void forward_launch(const NormArgs& a, int sms, cudaStream_t st) {
+  auto grid = [&](int64_t rows_a_block, int64_t blocks_an_sm) {
+    const int64_t n = ceil_div(a.rows, rows_a_block), most = sms * blocks_an_sm;
+    return (unsigned)(n < most ? n : most);
+  };
+  const int threads = block_threads(a.cols);
+  if (a.cols <= kWarpCols)
+    by_lanes(a.cols, [&](auto e, auto lanes) {
+      constexpr int kE = decltype(e)::value, kTpr = decltype(lanes)::value;
+      constexpr auto k = norm_forward_kernel<T, float, VEC, kE, kTpr>;
+      const size_t smem = Rows<T, VEC, kE, kRowSlots<T, kE>>::bytes(kThreads) + 2 * 4 * kE * kTpr;
+      k<<<grid(kThreads / kTpr, resident_blocks<k>(kThreads, smem)), kThreads, smem, st>>>(a);
+    });
+  else if (threads <= kBlockThreads) {
+    const size_t smem = Rows<T, VEC, kBlockElems, kRowSlots<T, kBlockElems>>::bytes(threads);
+    by_weight(a.w_bf16, [&](auto w) {
+      constexpr auto k = norm_forward_kernel<T, decltype(w), VEC, kBlockElems, 0>;
+      k<<<grid(1, resident_blocks<k>(threads, smem)), threads, smem, st>>>(a);
+    });
+  } else {
+    norm_forward_wide_kernel<T, VEC><<<grid(1, 4), kWideThreads, 0, st>>>(a);
   }
-  const int groups = groups_of(s.tpr), threads = groups * s.tpr;
-  int64_t grid = ceil_div(a.rows, groups);
-  const int64_t most = (int64_t)sms * (1024 / threads > 0 ? 1024 / threads : 1);
-  if (grid > most) grid = most;
-  if (s.e == 8) norm_forward_kernel<T, VEC, 8><<<(unsigned)grid, threads, 0, st>>>(a);
-  else norm_forward_kernel<T, VEC, 16><<<(unsigned)grid, threads, 0, st>>>(a);
 }
 
 // Blocks of the backward pass, shared out over the workers by their rows: a
@@ -442,30 +584,42 @@ int block_share(int n_workers, const int64_t* row_begin, int groups, int most, W
   return n;
 }
 
-constexpr int kBwdBlocksPerSm = 2;
+constexpr int kBwdBlocksPerSm = 8;
 // Of blocks at most: those of every SM, and one more for each worker whose
 // share rounds to none.
 int bwd_max_blocks(int sms, int n_workers) { return sms * kBwdBlocksPerSm + n_workers; }
 
 template <typename T, int VEC>
-void backward_launch(const NormArgs& a, RowShape s, const WorkerRows& rows, const int64_t* row_begin, int sms,
-                     WorkerBlocks* share, cudaStream_t st) {
-  if (!s.e) {
-    block_share(a.n_workers, row_begin, 64, sms, share);
-    const int blocks = share->begin[a.n_workers];
-    const int64_t grid = a.rows < (int64_t)sms * 4 ? a.rows : (int64_t)sms * 4;
-    if (a.rows) {
-      norm_backward_wide_kernel<T, VEC><<<(unsigned)grid, kWideThreads, 0, st>>>(a);
-      norm_columns_kernel<T><<<dim3((unsigned)blocks, (unsigned)ceil_div(a.cols, 32)), 256, 0, st>>>(a, rows, *share);
-    }
-    return;
+void backward_launch(const NormArgs& a, const WorkerRows& rows, const int64_t* row_begin, int sms, WorkerBlocks* share,
+                     cudaStream_t st) {
+  auto blocks = [&](int rows_a_block, int blocks_an_sm) {
+    return block_share(a.n_workers, row_begin, rows_a_block,
+                       sms * (blocks_an_sm < kBwdBlocksPerSm ? blocks_an_sm : kBwdBlocksPerSm), share);
+  };
+  const int threads = block_threads(a.cols);
+  if (!a.rows) return;
+  if (a.cols <= kWarpCols)
+    by_lanes(a.cols, [&](auto e, auto lanes) {
+      constexpr int kE = decltype(e)::value, kTpr = decltype(lanes)::value;
+      constexpr auto k = norm_backward_kernel<T, float, VEC, kE, kTpr>;
+      const size_t rings = 2 * Rows<T, VEC, kE, kRowSlots<T, 2 * kE>>::bytes(kThreads) + 4 * kE * kTpr;
+      const size_t sums = 4 * kThreads * kE, smem = rings > sums ? rings : sums;
+      const int n = blocks(kThreads / kTpr, resident_blocks<k>(kThreads, smem));
+      k<<<n, kThreads, smem, st>>>(a, rows, *share);
+    });
+  else if (threads <= kBlockThreads) {
+    const size_t smem = 2 * Rows<T, VEC, kBlockElems, kRowSlots<T, 2 * kBlockElems>>::bytes(threads);
+    by_weight(a.w_bf16, [&](auto w) {
+      constexpr auto k = norm_backward_kernel<T, decltype(w), VEC, kBlockElems, 0>;
+      const int n = blocks(1, resident_blocks<k>(threads, smem));
+      k<<<n, threads, smem, st>>>(a, rows, *share);
+    });
+  } else {
+    const int64_t most = (int64_t)sms * 4;
+    norm_backward_wide_kernel<T, VEC><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
+    const int n = blocks(64, 1);
+    norm_columns_kernel<T><<<dim3((unsigned)n, (unsigned)ceil_div(a.cols, 32)), 256, 0, st>>>(a, rows, *share);
   }
-  const int groups = groups_of(s.tpr), threads = groups * s.tpr;
-  const int blocks = block_share(a.n_workers, row_begin, groups, sms * kBwdBlocksPerSm, share);
-  if (!blocks) return;
-  const size_t smem = groups > 1 ? (size_t)(a.has_bias ? 2 : 1) * a.cols * 4 : 0;  // at most 16 KB
-  if (s.e == 8) norm_backward_kernel<T, VEC, 8><<<blocks, threads, smem, st>>>(a, rows, *share);
-  else norm_backward_kernel<T, VEC, 16><<<blocks, threads, smem, st>>>(a, rows, *share);
 }
 
 template <typename F>
@@ -500,10 +654,8 @@ signmuon_status signmuon_layer_norm_forward(int64_t rows, int32_t cols, signmuon
   NormArgs a = {};
   a.rows = rows, a.cols = cols, a.x = x, a.out = y, a.ld_x = ld_x, a.ld_out = ld_y, a.w = weight, a.b = bias;
   a.w_bf16 = w_dtype == SIGNMUON_BF16, a.eps = eps, a.mean = mean, a.rstd = rstd;
-  const RowShape s = row_shape(cols, kMaxThreads, vec);
-  a.tpr = s.tpr;
   by_vec(x_dtype, vec, [&](auto t, auto v) {
-    forward_launch<decltype(t), decltype(v)::value>(a, s, current_sms(), static_cast<cudaStream_t>(stream));
+    forward_launch<decltype(t), decltype(v)::value>(a, current_sms(), static_cast<cudaStream_t>(stream));
   });
   return cuda_status(cudaGetLastError());
 }
@@ -551,14 +703,12 @@ signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const 
   a.w = weight, a.w_bf16 = w_dtype == SIGNMUON_BF16, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeaderBytes);
   a.n_workers = n_workers, a.has_bias = dbias != nullptr;
-  const RowShape s = row_shape(cols, kBwdThreads, vec);
-  a.tpr = s.tpr;
   WorkerRows rows = {};
   for (int m = 0; m <= n_workers; ++m) rows.begin[m] = row_begin[m];
   WorkerBlocks share = {};
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   by_vec(x_dtype, vec, [&](auto t, auto v) {
-    backward_launch<decltype(t), decltype(v)::value>(a, s, rows, row_begin, current_sms(), &share, cs);
+    backward_launch<decltype(t), decltype(v)::value>(a, rows, row_begin, current_sms(), &share, cs);
   });
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);

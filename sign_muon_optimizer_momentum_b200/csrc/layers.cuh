@@ -3,6 +3,7 @@
 // host-side checks of their entry points.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -74,6 +75,22 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   typename RawVec<T, VEC>::type r;
   pack(v, r);
   *reinterpret_cast<typename RawVec<T, VEC>::type*>(p) = r;
+}
+
+// Asynchronous copies of 4 or 16 bytes to shared memory, seen by the thread
+// that issued them once its group is waited for.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* smem, const void* global) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(smem);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(global) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(global), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int bf16) {
@@ -153,12 +170,38 @@ inline int vec_narrow(int vec, signmuon_dtype t, const void* p, int64_t ld) {
   return vec;
 }
 
+// What is asked of the device once and kept: a few driver queries cost as
+// much as a small launch.
+constexpr int kMaxDevices = 64;
+inline int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : 0;
+}
 // SMs of the current device (148 on B200; 148 if the query fails).
 inline int current_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
+  static std::atomic<int> known[kMaxDevices];
+  const int dev = current_device();
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+// Allows kernel K all the dynamic shared memory there is (227 KB less its
+// static arrays), on this device, and gives the blocks of it that an SM holds.  `smem` is a function of K and `threads`.
+template <auto K>
+int resident_blocks(int threads, size_t smem) {
+  static std::atomic<int> known[kMaxDevices][33];
+  std::atomic<int>& slot = known[current_device()][threads / 32];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, K) == cudaSuccess)
+      cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - (int)attr.sharedSizeBytes);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, K, threads, smem) != cudaSuccess || n < 1) n = 1;
+    slot.store(n, std::memory_order_relaxed);
+  }
   return n;
 }
 

@@ -27,6 +27,7 @@ ValueError, failures in the library SignMuonError.
 from __future__ import annotations
 
 import contextlib
+import math
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -46,7 +47,14 @@ def _on(t: torch.Tensor):
 
 
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # torch.cuda.current_stream(t.device).cuda_stream without the Stream
+    # object, which takes as long to make as a small launch.
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _cuda(t: torch.Tensor, what: str, like: Optional[torch.Tensor] = None) -> None:
@@ -111,14 +119,16 @@ def _shares(rows: int, n_workers: int, splits: Optional[Sequence[int]]):
     return L._offsets(splits)
 
 
-def _per_worker(n_workers: int, shape: Tuple[int, ...], dtype: torch.dtype, device) -> List[torch.Tensor]:
-    """One tensor per worker, each 16-byte aligned as the step wants them."""
-    n = 1
-    for s in shape:
-        n *= s
-    if n_workers == 1 or n * dtype.itemsize % 16 == 0:
-        return list(torch.empty((n_workers, *shape), dtype=dtype, device=device).unbind(0))
-    return [torch.empty(shape, dtype=dtype, device=device) for _ in range(n_workers)]
+def _per_worker(n: int, shape: Tuple[int, ...], dtype: torch.dtype, device) -> Tuple[List[torch.Tensor], List[int]]:
+    """n tensors, each 16-byte aligned as the step wants them, and their
+    addresses."""
+    nbytes = math.prod(shape) * dtype.itemsize
+    if n == 1 or nbytes % 16 == 0:
+        whole = torch.empty((n, *shape), dtype=dtype, device=device)
+        p = whole.data_ptr()
+        return list(whole.unbind(0)), [p + i * nbytes for i in range(n)]
+    out = [torch.empty(shape, dtype=dtype, device=device) for _ in range(n)]
+    return out, [g.data_ptr() for g in out]
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -174,7 +184,7 @@ def embedding_backward(ids: torch.Tensor, grad_out: torch.Tensor, vocab: int, n_
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = _per_worker(n_workers, (vocab, cols), dtype, grad_out.device)
+        out, ptrs = _per_worker(n_workers, (vocab, cols), dtype, grad_out.device)
     else:
         out = list(out)
         if len(out) != n_workers:
@@ -183,10 +193,11 @@ def embedding_backward(ids: torch.Tensor, grad_out: torch.Tensor, vocab: int, n_
             _matrix(g, (vocab, cols), dtype, f"out[{m}]", grad_out)
             if not g.is_contiguous():
                 raise ValueError(f"out[{m}] must be contiguous")
+        ptrs = [g.data_ptr() for g in out]
     with _on(grad_out):
         ws = _workspace(L.signmuon_embedding_backward_workspace_bytes((vocab, cols), shares), grad_out.device)
         L.signmuon_embedding_backward((vocab, cols), shares, wide, ids.data_ptr(), code, grad_out.data_ptr(), ld, scale,
-                                      accumulate, grad_code, [g.data_ptr() for g in out], ws.data_ptr(), ws.numel(),
+                                      accumulate, grad_code, ptrs, ws.data_ptr(), ws.numel(),
                                       _stream(grad_out))
     return out
 
@@ -215,7 +226,7 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[tor
         raise ValueError("eps must be >= 0")
     code, w_code = _dtype_code(x.dtype), _dtype_code(weight.dtype)
     if out is None:
-        out, ld_y = torch.empty(x.shape, dtype=x.dtype, device=x.device), cols
+        out, ld_y = _like(x), cols
     else:
         ld_y = _matrix(out, x.shape, x.dtype, "out", x)
     mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device).unbind(0)
@@ -252,16 +263,16 @@ def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.T
     code, w_code = _dtype_code(x.dtype), _dtype_code(weight.dtype)
     shares = _shares(rows, n_workers, splits)
     if out is None:
-        out, ld_dx = torch.empty(x.shape, dtype=x.dtype, device=x.device), cols
+        out, ld_dx = _like(x), cols
     else:
         ld_dx = _matrix(out, x.shape, x.dtype, "out", x)
-    grads = _per_worker(n_workers * (2 if bias else 1), tuple(weight.shape), weight.dtype, x.device)
+    grads, ptrs = _per_worker(n_workers * (2 if bias else 1), weight.shape, weight.dtype, x.device)
     dw, db = grads[:n_workers], grads[n_workers:] if bias else None
     with _on(x):
         ws = _workspace(L.signmuon_layer_norm_backward_workspace_bytes(cols, shares), x.device)
         L.signmuon_layer_norm_backward(cols, shares, code, grad_out.data_ptr(), ld_dy, x.data_ptr(), ld_x, w_code,
                                        weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), ld_dx,
-                                       [g.data_ptr() for g in dw], [g.data_ptr() for g in db] if bias else None,
+                                       ptrs[:n_workers], ptrs[n_workers:] if bias else None,
                                        ws.data_ptr(), ws.numel(), _stream(x))
     return out, dw, db
 
@@ -288,7 +299,7 @@ def _distill(logits, top_ids, top_logits, n_workers, splits, temperature, grad_s
     ld_d = 0
     if with_grad:
         if out is None:
-            out, ld_d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), vocab
+            out, ld_d = _like(logits), vocab
         else:
             ld_d = _matrix(out, logits.shape, logits.dtype, "out", logits)
     with _on(logits):
