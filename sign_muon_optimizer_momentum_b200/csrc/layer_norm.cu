@@ -8,31 +8,37 @@
 //              dw[m] = sum over worker m's rows of dy xh,  db[m] = sum of dy
 //
 // All of it is bound by memory: forward reads x and writes y, backward reads
-// x and dy and writes dx, each once.  A row is held in the registers of the
-// group of threads that works on it (kE elements a thread), so both of the
-// variance's passes and the backward's two sums cost no second read; groups
-// walk over rows, and each thread keeps its part of the next rows coming by
-// asynchronous copies into a ring of its own in shared memory (no barrier:
-// a thread reads back only what it copied).  The backward adds dy xh
-// and dy of its rows to per-thread column sums, adds those of a block's groups
-// in shared memory, and leaves one row of partial sums a block; a second
-// launch adds a worker's blocks.  All sums have a fixed order.
+// x and dy and writes dx, each once.  A row is held in the registers of kTpr
+// threads (a part of a warp, a warp, or several warps),
+// so both of the variance's passes and the backward's two sums cost no second
+// read; each group of threads walks over rows, and each thread keeps its part
+// of the next rows coming by asynchronous copies into a ring of its own in
+// shared memory (no barrier: a thread reads back only what it copied).
+//
+// Rows of any length are read and written 16 bytes at a time.  Where a row's
+// stride is not a multiple of that, rows start at different places within 16
+// bytes, the same place again after `period` rows: a block takes only rows
+// that start at the same place (`shift` elements into their first 16 bytes),
+// so that a thread keeps its columns and masks for the whole call.
+//
+// The backward adds dy xh and dy of its rows to per-thread column sums, adds
+// those of a block's groups in shared memory, and leaves one row of partial
+// sums a block; a second launch adds a worker's blocks.  All sums have a fixed
+// order.
 #include "layers.cuh"
 
 using namespace signmuon;
 
 namespace {
 
-constexpr int kWarpCols = 1024;       // longest row that one warp takes (32 elements a lane)
-constexpr int kThreads = 256;         // threads a block where a warp or less takes a row
-constexpr int kBlockElems = 16;       // elements a thread where a block takes a row
-constexpr int kBlockThreads = 512;    // threads of such a block at most (8192 columns)
-constexpr int kWideThreads = 512;     // rows longer still
+constexpr int kThreads = 256;         // threads a block for rows of up to that many
+constexpr int kWideThreads = 512;     // threads a block for rows that registers do not hold
 
 // Rows and columns of one call.
 struct NormArgs {
   int64_t rows;
   int32_t cols;
+  int32_t period;                     // rows after which starts within 16 bytes repeat
   const void* x;
   const void* dy;
   void* out;                          // y or dx
@@ -46,49 +52,82 @@ struct NormArgs {
   float* part;                        // backward: [blocks][sums][cols]
   int32_t n_workers, has_bias;
 };
-// A thread's part of a row: chunk c is the VEC elements from column
-// (c * tpr + t) * VEC, tpr threads to a row.  Rows come through kSlots slots
-// of shared memory; single bf16 (2 bytes, below what can be copied
-// asynchronously) are loaded when they are needed.
-template <typename T, int VEC, int E, int kSlots>
+
+// What a thread has of a row: chunk c is the VEC elements from column
+// col(c) = (c * kTpr + t) * VEC - shift.  Bit i of `mask` says whether element
+// i is in the row: some of the first chunk of a row may lie before it, some of
+// the last after it, unless rows start on 16 bytes and end with a chunk
+// (kWhole).
+template <int VEC, int E, int kTpr, bool kWhole>
+struct Part {
+  int t, cols, shift;
+  uint32_t mask;
+  __device__ __forceinline__ Part(int t, int cols, int shift) : t(t), cols(cols), shift(kWhole ? 0 : shift), mask(0) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int at = col(i / VEC) + i % VEC;
+      mask |= at >= 0 && at < cols ? 1u << i : 0u;
+    }
+  }
+  __device__ __forceinline__ int col(int c) const { return (c * kTpr + t) * VEC - (kWhole ? 0 : shift); }
+  __device__ __forceinline__ bool in(int c, int j) const { return mask >> (c * VEC + j) & 1; }
+  __device__ __forceinline__ bool any(int c) const { return kWhole || VEC == 1 ? in(c, 0) : (mask >> c * VEC & kFull) != 0; }
+  __device__ __forceinline__ bool whole(int c) const { return kWhole || VEC == 1 ? in(c, 0) : (mask >> c * VEC & kFull) == kFull; }
+  // The same, with tests of the mask to be made where they are used: their
+  // results, kept over the loop over rows, would take more registers than the
+  // row.
+  __device__ __forceinline__ Part again() const {
+    Part p = *this;
+    asm volatile("" : "+r"(p.mask));
+    return p;
+  }
+  static constexpr uint32_t kFull = (1u << VEC) - 1;
+};
+
+// Rows come through kSlots slots of shared memory; single bf16 (2 bytes, below
+// what can be copied asynchronously) are loaded when they are needed.
+template <typename T, int VEC, int E, int kTpr, bool kWhole, int kSlots, int kBlock>
 struct Rows {
   using Raw = typename RawVec<T, VEC>::type;
+  using P = Part<VEC, E, kTpr, kWhole>;
   static constexpr int kChunks = E / VEC;
   static constexpr bool kAsync = sizeof(Raw) >= 4;
-  static constexpr size_t bytes(int threads) { return kAsync ? (size_t)kSlots * kChunks * sizeof(Raw) * threads : 0; }
+  static constexpr size_t kBytes = kAsync ? (size_t)kSlots * kChunks * sizeof(Raw) * kBlock : 0;
   Raw* ring;
-  int t, tpr, cols;
-  // Slots past the last column are 0 from the start and stay so.
-  __device__ __forceinline__ Rows(void* smem, int t, int tpr, int cols)
-      : ring(static_cast<Raw*>(smem) + threadIdx.x), t(t), tpr(tpr), cols(cols) {
+  // Slots without columns are 0 from the start and stay so.
+  __device__ __forceinline__ Rows(void* smem, const P& p) : ring(static_cast<Raw*>(smem) + threadIdx.x) {
     if constexpr (kAsync) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
-        if ((c * tpr + t) * VEC >= cols)
+        if (!p.any(c))
 #pragma unroll
-          for (int i = 0; i < kSlots; ++i) ring[(i * kChunks + c) * blockDim.x] = Raw{};
+          for (int i = 0; i < kSlots; ++i) ring[(i * kChunks + c) * kBlock] = Raw{};
     }
   }
-  __device__ __forceinline__ void fetch(const T* p, int slot) const {
+  __device__ __forceinline__ void fetch(const P& p, const T* row, int slot) const {
     if constexpr (kAsync) {
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int col = (c * tpr + t) * VEC;
-        if (col < cols) copy_async<sizeof(Raw)>(ring + (slot * kChunks + c) * blockDim.x, p + col);
-      }
+      for (int c = 0; c < kChunks; ++c)
+        // What a chunk has after the row's end is not read, but zero.
+        if (p.any(c))
+          copy_async<sizeof(Raw), kWhole>(ring + (slot * kChunks + c) * kBlock, row + p.col(c),
+                                          min(VEC, p.cols - p.col(c)) * (int)sizeof(T));
     }
   }
-  // Elements past the last column are 0.
-  __device__ __forceinline__ void get(float (&v)[E], const T* p, int slot) const {
+  // The elements outside the row are 0.
+  __device__ __forceinline__ void get(const P& p, float (&v)[E], const T* row, int slot) const {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       float u[VEC];
       if constexpr (kAsync) {
-        unpack(ring[(slot * kChunks + c) * blockDim.x], u);
+        unpack(ring[(slot * kChunks + c) * kBlock], u);
+        if (!kWhole && c == 0 && !p.whole(0)) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) u[j] = p.in(0, j) ? u[j] : 0.f;
+        }
       } else {
-        const int col = (c * tpr + t) * VEC;
         u[0] = 0.f;
-        if (col < cols) unpack(load_stream<T, VEC>(p + col), u);
+        if (p.any(c)) unpack(load_stream<T, VEC>(row + p.col(c)), u);
       }
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[c * VEC + j] = u[j];
@@ -99,154 +138,180 @@ struct Rows {
 template <typename T, int E>
 constexpr int kRowSlots = 192 / (E * (int)sizeof(T)) < 2 ? 2 : 192 / (E * (int)sizeof(T)) > 4 ? 4 : 192 / (E * (int)sizeof(T));
 
-// A thread's weights (zero past the last column).  Where a block takes a row:
-// in registers, as they are stored (W is the type).  Where a warp or less
-// takes a row, a thread has too many for that: fp32 in shared memory, each
-// group of four of the kTpr lanes side by side, so that reads meet no bank
-// conflict (rows of eight by lane cost twice the reads, which then bound the
-// forward kernel).
-template <typename W, int VEC, int E>
-struct RegWeights {
-  static constexpr bool kBf16 = sizeof(W) == 2;
-  uint32_t reg[kBf16 ? E / 2 : E];
-  __device__ __forceinline__ void load(const void* w, int, float*, int t, int tpr, int cols) {
-    uint32_t v[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int col = (i / VEC * tpr + t) * VEC + i % VEC;
-      v[i] = w && col < cols ? __float_as_uint(load_elem(w, col, kBf16)) : 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < (kBf16 ? E / 2 : E); ++i) reg[i] = kBf16 ? v[2 * i % E] >> 16 | v[(2 * i + 1) % E] : v[i];
-  }
-  __device__ __forceinline__ void get(int c, float (&v)[VEC]) const {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int i = c * VEC + j;
-      if constexpr (kBf16) v[j] = i % 2 ? bf16_hi(reg[i / 2]) : bf16_lo(reg[i / 2]);
-      else v[j] = __uint_as_float(reg[i]);
-    }
-  }
-};
-template <int VEC, int E, int kTpr>
-struct SharedWeights {
-  const float* sh;  // this lane's first
-  __device__ __forceinline__ void load(const void* w, int bf16, float* smem, int t, int, int cols) {
-    // Element q of group g (of min(VEC, 4)) of chunk c of lane l.
-    for (int col = threadIdx.x; col < E * kTpr; col += kThreads) {
-      const int c = col / (kTpr * VEC), l = col / VEC % kTpr, j = col % VEC;
-      smem[at(c, j) + l * kGroup] = w && col < cols ? load_elem(w, col, bf16) : 0.f;
-    }
-    sh = smem + t * kGroup;
-  }
+// A thread's weights (zero outside the row): fp32 in shared memory, groups of
+// four of a row's threads side by side, so that reads meet no bank conflict.
+// (In registers they would halve the threads an SM holds; with a thread's
+// eight together, reads take twice as long and bound the forward kernel.)
+template <int VEC, int E, int kTpr, bool kWhole>
+struct Weights {
+  using P = Part<VEC, E, kTpr, kWhole>;
   static constexpr int kGroup = VEC < 4 ? VEC : 4;
-  __device__ __forceinline__ static int at(int c, int j) { return (c * (VEC / kGroup) + j / kGroup) * kTpr * kGroup + j % kGroup; }
+  static constexpr size_t kBytes = 4 * E * kTpr;
+  const float* sh;  // this thread's first
+  __device__ __forceinline__ Weights(void* smem, const P& p, const void* w, int bf16)
+      : sh(static_cast<float*>(smem) + p.t * kGroup) {
+    for (int i = threadIdx.x; i < E * kTpr; i += blockDim.x) {
+      const int j = i % VEC, l = i / VEC % kTpr, c = i / VEC / kTpr, col = i - p.shift;
+      static_cast<float*>(smem)[at(c, j) + l * kGroup] = w && col >= 0 && col < p.cols ? load_elem(w, col, bf16) : 0.f;
+    }
+  }
+  __device__ __forceinline__ static constexpr int at(int c, int j) {
+    return (c * (VEC / kGroup) + j / kGroup) * kTpr * kGroup + j % kGroup;
+  }
   __device__ __forceinline__ void get(int c, float (&v)[VEC]) const {
 #pragma unroll
     for (int j = 0; j < VEC; j += kGroup) {
       if constexpr (kGroup == 4) {
         const float4 q = *reinterpret_cast<const float4*>(sh + at(c, j));
         v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
-      } else if constexpr (kGroup == 2) {
-        const float2 q = *reinterpret_cast<const float2*>(sh + at(c, j));
-        v[j] = q.x, v[j + 1] = q.y;
       } else {
         v[j] = sh[at(c, j)];
       }
     }
   }
 };
-template <typename W, int VEC, int E, int kTpr>
-using Weights = std::conditional_t<kTpr == 0, RegWeights<W, VEC, E>, SharedWeights<VEC, E, kTpr>>;
 
-// Sum over the kTpr lanes of a row's group (kTpr <= 32), or over the block
-// (kTpr == 0) by way of sh.  Blocks alternate between two arrays, so that one
-// barrier a sum does.
-template <int kTpr>
-__device__ __forceinline__ float row_sum(float v, float* sh) {
+// Sums of N values over the kTpr threads of a row.  Groups of more than a warp
+// exchange their warps' sums by `sh`, one of two arrays that a caller uses in
+// turn: then one barrier a sum does.
+template <int kTpr, int N>
+struct RowSum {
+  static constexpr int kWarps = kTpr / 32;
+  struct Shared {
+    float warp[2][kTpr > kThreads ? kTpr / 32 : kThreads / 32][N];
+  };
+  __device__ __forceinline__ static void run(float (&v)[N], Shared& sh, int turn) {
 #pragma unroll
-  for (int o = (kTpr ? kTpr : 32) / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (kTpr == 0) {
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x / 32] = v;
-    __syncthreads();
-    const float4* q = reinterpret_cast<const float4*>(sh);
-    v = 0.f;
-    for (int i = 0; i < (int)blockDim.x / 32; i += 4) {
-      const float4 p = q[i / 4];  // zero past the block's warps
-      v += (p.x + p.y) + (p.z + p.w);
+    for (int o = (kTpr < 32 ? kTpr : 32) / 2; o; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    if constexpr (kTpr > 32) {
+      const int group = threadIdx.x / kTpr, warp = threadIdx.x / 32;
+      if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int n = 0; n < N; ++n) sh.warp[turn][warp][n] = v[n];
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kTpr) : "memory");
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i)
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] += sh.warp[turn][group * kWarps + i][n];
     }
   }
-  return v;
+};
+
+// Writes a chunk: whole chunks at once, the ends of a row by elements.
+template <typename T, int VEC, int E, int kTpr, bool kWhole>
+__device__ __forceinline__ void store_chunk(const Part<VEC, E, kTpr, kWhole>& p, T* row, int c, const float (&o)[VEC]) {
+  if (kWhole || VEC == 1 || p.whole(c)) {
+    store_stream<T, VEC>(row + p.col(c), o);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (p.in(c, j)) store_elem(row, p.col(c) + j, sizeof(T) == 2, o[j]);
+  }
 }
 
 // --------------------------------------------------------------- forward
-// kTpr lanes (8, 16 or 32) a row, or 0: a block a row.  The variance is taken
-// about the mean, from the values in registers.
-template <typename T, typename W, int VEC, int E, int kTpr>
-__global__ void __launch_bounds__(kTpr ? kThreads : kBlockThreads) norm_forward_kernel(const NormArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) float sh[2][kBlockThreads / 32];
-  constexpr bool kBlock = kTpr == 0;
+// The variance is taken about the mean, from the values in registers.
+template <typename T, int VEC, int E, int kTpr, bool kWhole>
+struct Forward {
+  static constexpr int kBlock = kTpr > kThreads ? kTpr : kThreads, kGroups = kBlock / kTpr;
+  using Ring = Rows<T, VEC, E, kTpr, kWhole, kRowSlots<T, E>, kBlock>;
+  using W = Weights<VEC, E, kTpr, kWhole>;
+  static constexpr size_t kSmem = Ring::kBytes + 2 * W::kBytes;
+};
+template <typename T, int VEC, int E, int kTpr, bool kWhole>
+__global__ void __launch_bounds__(kTpr > kThreads ? kTpr : kThreads, VEC > 1 && kTpr >= 64 && kTpr <= kThreads && E == 32 ? 4 : 1)
+norm_forward_kernel(const NormArgs a) {
+  using F = Forward<T, VEC, E, kTpr, kWhole>;
+  using Sum = RowSum<kTpr, 1>;
   constexpr int kSlots = kRowSlots<T, E>;
-  const int tpr = kBlock ? blockDim.x : kTpr, t = threadIdx.x % tpr, cols = a.cols;
-  constexpr int groups = kBlock ? 1 : kThreads / (kBlock ? 1 : kTpr);
-  const float inv_cols = 1.f / (float)cols;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ typename Sum::Shared sh;
+  // Each of a period's blocks takes rows that start at the same place.
+  const int64_t step = (int64_t)(gridDim.x / a.period) * F::kGroups * a.period;
+  const int64_t row0 = (int64_t)(blockIdx.x / a.period) * F::kGroups * a.period + blockIdx.x % a.period;
+  const float inv_cols = 1.f / (float)a.cols;
   const T* x = static_cast<const T*>(a.x);
   T* y = static_cast<T*>(a.out);
+  // All threads of a warp run the same iterations (`first` is the row of the
+  // warp's first thread); rows past the end are masked.
+  int64_t row = row0 + (int64_t)(threadIdx.x / kTpr) * a.period;
+  int64_t first = row0 + (int64_t)(threadIdx.x / 32 * 32 / kTpr) * a.period;
+  const Part<VEC, E, kTpr, kWhole> part_of(threadIdx.x % kTpr, a.cols, (int)(row0 * a.ld_x % VEC));
 
-  // All lanes of a warp run the same iterations (`first` is the row of the
-  // warp's first lane); rows past the end are masked.
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row = (int64_t)blockIdx.x * groups + threadIdx.x / tpr;
-  int64_t first = (int64_t)blockIdx.x * groups + threadIdx.x / 32 * 32 / tpr;
-  const Rows<T, VEC, E, kSlots> in(smem, t, tpr, cols);
+  const typename F::Ring in(smem, part_of);
 #pragma unroll
   for (int i = 0; i < kSlots - 1; ++i) {
-    if (row + i * step < a.rows) in.fetch(x + (row + i * step) * a.ld_x, i);
+    if (row + i * step < a.rows) in.fetch(part_of, x + (row + i * step) * a.ld_x, i);
     copy_commit();
   }
-  float* w_sh = reinterpret_cast<float*>(smem + Rows<T, VEC, E, kSlots>::bytes(blockDim.x));
-  Weights<W, VEC, E, kTpr> w, b;
-  w.load(a.w, a.w_bf16, w_sh, t, tpr, cols);
-  b.load(a.b, a.w_bf16, w_sh + E * kTpr, t, tpr, cols);
-  if (threadIdx.x < 2 * kBlockThreads / 32) sh[0][threadIdx.x] = 0.f;
+  const typename F::W w(smem + F::Ring::kBytes, part_of, a.w, a.w_bf16);
+  const typename F::W b(smem + F::Ring::kBytes + F::W::kBytes, part_of, a.b, a.w_bf16);
   __syncthreads();
 
   int slot = 0;
   for (; first < a.rows; row += step, first += step) {
+    const auto p = part_of.again();
     const int64_t ahead = row + (kSlots - 1) * step;
-    if (ahead < a.rows) in.fetch(x + ahead * a.ld_x, slot == 0 ? kSlots - 1 : slot - 1);
+    if (ahead < a.rows) in.fetch(p, x + ahead * a.ld_x, slot == 0 ? kSlots - 1 : slot - 1);
     copy_commit();
     copy_wait<kSlots - 1>();
     const bool valid = row < a.rows;
-    float v[E];
-    in.get(v, x + (valid ? row : 0) * a.ld_x, slot);
+    float u[E];
+    in.get(p, u, x + (valid ? row : 0) * a.ld_x, slot);
     slot = slot == kSlots - 1 ? 0 : slot + 1;
-    float s = 0.f;
+    Pair v[E / 2], sum(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < E; ++i) s += v[i];
-    const float mean = row_sum<kTpr>(s, sh[0]) * inv_cols;
-    s = 0.f;
-#pragma unroll
-    for (int c = 0; c < E / VEC; ++c)
-      if ((c * tpr + t) * VEC < cols)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          v[c * VEC + j] -= mean;
-          s = fmaf(v[c * VEC + j], v[c * VEC + j], s);
-        }
-    const float r = rsqrtf(row_sum<kTpr>(s, sh[1]) * inv_cols + a.eps);
-    if (t == 0 && valid) a.mean[row] = mean, a.rstd[row] = r;
+    for (int i = 0; i < E / 2; ++i) v[i] = Pair(u[2 * i], u[2 * i + 1]), sum = sum + v[i];
+    float s[1] = {sum.lo() + sum.hi()};
+    Sum::run(s, sh, 0);
+    const float mean = s[0] * inv_cols;
+    const Pair minus(-mean, -mean);
+    sum = Pair(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < E / VEC; ++c) {
-      const int col = (c * tpr + t) * VEC;
-      if (col < cols && valid) {
+      if constexpr (VEC == 1) {
+        if (c % 2 == 0) {
+          v[c / 2] = v[c / 2] + minus;
+          v[c / 2] = Pair(p.any(c) ? v[c / 2].lo() : 0.f, p.any(c + 1) ? v[c / 2].hi() : 0.f);
+          sum = fma(v[c / 2], v[c / 2], sum);
+        }
+      } else if (p.any(c)) {
+        const bool whole = kWhole || p.whole(c);
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+          Pair& q = v[(c * VEC + j) / 2];
+          q = q + minus;
+          if (!whole) q = Pair(p.in(c, j) ? q.lo() : 0.f, p.in(c, j + 1) ? q.hi() : 0.f);
+          sum = fma(q, q, sum);
+        }
+      }
+    }
+    s[0] = sum.lo() + sum.hi();
+    Sum::run(s, sh, 1);
+    const float r = rsqrtf(s[0] * inv_cols + a.eps);
+    if (p.t == 0 && valid) a.mean[row] = mean, a.rstd[row] = r;
+    const Pair rr(r, r);
+    T* out = y + row * a.ld_out;
+#pragma unroll
+    for (int c = 0; c < E / VEC; ++c) {
+      if (p.any(c) && valid) {
         float o[VEC], wv[VEC], bv[VEC];
         w.get(c, wv);
         b.get(c, bv);
+        if constexpr (VEC == 1) {
+          o[0] = fmaf((c % 2 ? v[c / 2].hi() : v[c / 2].lo()) * r, wv[0], bv[0]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = fmaf(v[c * VEC + j] * r, wv[j], bv[j]);
-        store_stream<T, VEC>(y + row * a.ld_out + col, o);
+          for (int j = 0; j < VEC; j += 2) {
+            const Pair q = fma(v[(c * VEC + j) / 2] * rr, Pair(wv[j], wv[j + 1]), Pair(bv[j], bv[j + 1]));
+            o[j] = q.lo(), o[j + 1] = q.hi();
+          }
+        }
+        store_chunk<T>(p, out, c, o);
       }
     }
   }
@@ -298,137 +363,163 @@ __global__ void __launch_bounds__(kWideThreads) norm_forward_wide_kernel(const N
 }
 
 // -------------------------------------------------------------- backward
-template <typename T, typename W, int VEC, int E, int kTpr>
-__global__ void __launch_bounds__(kTpr ? kThreads : kBlockThreads)
+template <typename T, int VEC, int E, int kTpr, bool kWhole>
+struct Backward {
+  static constexpr int kBlock = kTpr > kThreads ? kTpr : kThreads, kGroups = kBlock / kTpr;
+  using Ring = Rows<T, VEC, E, kTpr, kWhole, kRowSlots<T, 2 * E>, kBlock>;
+  using W = Weights<VEC, E, kTpr, kWhole>;
+  static constexpr size_t kRun = 2 * Ring::kBytes + W::kBytes, kSums = kGroups > 1 ? 4 * kBlock * E : 0;
+  static constexpr size_t kSmem = kRun > kSums ? kRun : kSums;
+};
+template <typename T, int VEC, int E, int kTpr, bool kWhole>
+__global__ void __launch_bounds__(kTpr > kThreads ? kTpr : kThreads)
 norm_backward_kernel(const NormArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks share) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) float sh[2][2][kBlockThreads / 32];
-  constexpr bool kBlock = kTpr == 0;
+  using B = Backward<T, VEC, E, kTpr, kWhole>;
+  using Sum = RowSum<kTpr, 2>;
+  using Ring = typename B::Ring;
   constexpr int kSlots = kRowSlots<T, 2 * E>;
-  const int tpr = kBlock ? blockDim.x : kTpr, t = threadIdx.x % tpr, cols = a.cols;
-  constexpr int groups = kBlock ? 1 : kThreads / (kBlock ? 1 : kTpr);
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ typename Sum::Shared sh;
   const int m = worker_of_block(share, a.n_workers, blockIdx.x);
-  const int blocks = share.begin[m + 1] - share.begin[m];
-  const float inv_cols = 1.f / (float)cols;
+  const int blocks = share.begin[m + 1] - share.begin[m], mine = blockIdx.x - share.begin[m];
+  const float inv_cols = 1.f / (float)a.cols;
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
   T* dx = static_cast<T*>(a.out);
+  const int64_t step = (int64_t)(blocks / a.period) * B::kGroups * a.period, end = rows.begin[m + 1];
+  const int64_t row0 = rows.begin[m] + (int64_t)(mine / a.period) * B::kGroups * a.period + mine % a.period;
+  int64_t row = row0 + (int64_t)(threadIdx.x / kTpr) * a.period;
+  int64_t first = row0 + (int64_t)(threadIdx.x / 32 * 32 / kTpr) * a.period;
+  const Part<VEC, E, kTpr, kWhole> part_of(threadIdx.x % kTpr, a.cols, (int)(row0 * a.ld_x % VEC));
 
-  const int64_t step = (int64_t)blocks * groups, end = rows.begin[m + 1];
-  int64_t first = rows.begin[m] + (int64_t)(blockIdx.x - share.begin[m]) * groups;
-  int64_t row = first + threadIdx.x / tpr;
-  first += threadIdx.x / 32 * 32 / tpr;
-  using Ring = Rows<T, VEC, E, kSlots>;
-  const Ring in_x(smem, t, tpr, cols), in_g(smem + Ring::bytes(blockDim.x), t, tpr, cols);
+  const Ring in_x(smem, part_of), in_g(smem + Ring::kBytes, part_of);
 #pragma unroll
   for (int i = 0; i < kSlots - 1; ++i) {
-    if (row + i * step < end) in_x.fetch(x + (row + i * step) * a.ld_x, i), in_g.fetch(dy + (row + i * step) * a.ld_dy, i);
+    const int64_t at = row + i * step;
+    if (at < end) in_x.fetch(part_of, x + at * a.ld_x, i), in_g.fetch(part_of, dy + at * a.ld_dy, i);
     copy_commit();
   }
   float mean_next = 0.f, r_next = 0.f;
   if (row < end) mean_next = a.mean[row], r_next = a.rstd[row];
-  Weights<W, VEC, E, kTpr> w;
-  w.load(a.w, a.w_bf16, reinterpret_cast<float*>(smem + 2 * Ring::bytes(blockDim.x)), t, tpr, cols);
-  if (threadIdx.x < 4 * kBlockThreads / 32) sh[0][0][threadIdx.x] = 0.f;
+  const typename B::W w(smem + 2 * Ring::kBytes, part_of, a.w, a.w_bf16);
   __syncthreads();
 
-  float dw[E], db[E];
+  Pair dw[E / 2], db[E / 2];
 #pragma unroll
-  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < E / 2; ++i) dw[i] = db[i] = Pair(0.f, 0.f);
   int slot = 0;
-  for (int it = 0; first < end; row += step, first += step, it ^= 1) {
+  for (int turn = 0; first < end; row += step, first += step, turn ^= 1) {
+    const auto p = part_of.again();
     const int64_t ahead = row + (kSlots - 1) * step;
     if (ahead < end) {
       const int to = slot == 0 ? kSlots - 1 : slot - 1;
-      in_x.fetch(x + ahead * a.ld_x, to), in_g.fetch(dy + ahead * a.ld_dy, to);
+      in_x.fetch(p, x + ahead * a.ld_x, to), in_g.fetch(p, dy + ahead * a.ld_dy, to);
     }
     copy_commit();
     const float mean = mean_next, r = r_next;
     if (row + step < end) mean_next = a.mean[row + step], r_next = a.rstd[row + step];
     copy_wait<kSlots - 1>();
     const bool valid = row < end;
-    float xh[E], g[E], s1 = 0.f, s2 = 0.f;
-    in_x.get(xh, x + (valid ? row : 0) * a.ld_x, slot);
-    in_g.get(g, dy + (valid ? row : 0) * a.ld_dy, slot);
+    Pair xh[E / 2], g[E / 2], s1(0.f, 0.f), s2(0.f, 0.f);
+    {
+      float u[E];
+      in_x.get(p, u, x + (valid ? row : 0) * a.ld_x, slot);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) xh[i] = Pair(u[2 * i], u[2 * i + 1]);
+      in_g.get(p, u, dy + (valid ? row : 0) * a.ld_dy, slot);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) g[i] = Pair(u[2 * i], u[2 * i + 1]);
+    }
     slot = slot == kSlots - 1 ? 0 : slot + 1;
+    const Pair minus(-mean, -mean), rr(r, r);
 #pragma unroll
     for (int c = 0; c < E / VEC; ++c) {
-      const int col = (c * tpr + t) * VEC;
-      if (col < cols && valid) {
+      if constexpr (VEC == 1) {
+        if (c % 2 == 0 && p.any(c) && valid) {
+          float w0[1], w1[1];
+          w.get(c, w0), w.get(c + 1, w1);
+          const Pair q = (xh[c / 2] + minus) * rr;
+          xh[c / 2] = Pair(q.lo(), p.any(c + 1) ? q.hi() : 0.f);
+          db[c / 2] = db[c / 2] + g[c / 2];
+          dw[c / 2] = fma(g[c / 2], xh[c / 2], dw[c / 2]);
+          g[c / 2] = g[c / 2] * Pair(w0[0], w1[0]);
+          s1 = s1 + g[c / 2];
+          s2 = fma(g[c / 2], xh[c / 2], s2);
+        }
+      } else if (p.any(c) && valid) {
+        const bool whole = kWhole || p.whole(c);
         float wv[VEC];
         w.get(c, wv);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int i = c * VEC + j;
-          xh[i] = (xh[i] - mean) * r;
-          db[i] += g[i];
-          dw[i] = fmaf(g[i], xh[i], dw[i]);
-          g[i] *= wv[j];
-          s1 += g[i];
-          s2 = fmaf(g[i], xh[i], s2);
+        for (int j = 0; j < VEC; j += 2) {
+          const int i = (c * VEC + j) / 2;
+          xh[i] = (xh[i] + minus) * rr;
+          // Elements outside the row: xh may be anything there, dy is 0.
+          if (!whole) xh[i] = Pair(p.in(c, j) ? xh[i].lo() : 0.f, p.in(c, j + 1) ? xh[i].hi() : 0.f);
+          db[i] = db[i] + g[i];
+          dw[i] = fma(g[i], xh[i], dw[i]);
+          g[i] = g[i] * Pair(wv[j], wv[j + 1]);
+          s1 = s1 + g[i];
+          s2 = fma(g[i], xh[i], s2);
         }
       }
     }
-    if constexpr (kBlock) {
-      // Both sums with one barrier; the arrays alternate by rows.
-      s1 = warp_sum(s1);
-      s2 = warp_sum(s2);
-      if ((threadIdx.x & 31) == 0) sh[it][0][threadIdx.x / 32] = s1, sh[it][1][threadIdx.x / 32] = s2;
-      __syncthreads();
-      s1 = s2 = 0.f;
-      for (int i = 0; i < (int)blockDim.x / 32; i += 4) {
-        const float4 p = *reinterpret_cast<const float4*>(&sh[it][0][i]), q = *reinterpret_cast<const float4*>(&sh[it][1][i]);
-        s1 += (p.x + p.y) + (p.z + p.w);
-        s2 += (q.x + q.y) + (q.z + q.w);
-      }
-    } else {
-      s1 = row_sum<kTpr>(s1, nullptr);
-      s2 = row_sum<kTpr>(s2, nullptr);
-    }
-    const float c1 = -r * s1 * inv_cols, c2 = -r * s2 * inv_cols;
+    float s[2] = {s1.lo() + s1.hi(), s2.lo() + s2.hi()};
+    Sum::run(s, sh, turn);
+    const float c1 = -r * s[0] * inv_cols, c2 = -r * s[1] * inv_cols;
+    const Pair cc1(c1, c1), cc2(c2, c2);
+    T* out = dx + row * a.ld_out;
 #pragma unroll
     for (int c = 0; c < E / VEC; ++c) {
-      const int col = (c * tpr + t) * VEC;
-      if (col < cols && valid) {
+      if (p.any(c) && valid) {
         float o[VEC];
+        if constexpr (VEC == 1) {
+          const Pair q = fma(xh[c / 2], cc2, fma(g[c / 2], rr, cc1));
+          o[0] = c % 2 ? q.hi() : q.lo();
+        } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = fmaf(xh[c * VEC + j], c2, fmaf(g[c * VEC + j], r, c1));
-        store_stream<T, VEC>(dx + row * a.ld_out + col, o);
+          for (int j = 0; j < VEC; j += 2) {
+            const int i = (c * VEC + j) / 2;
+            const Pair q = fma(xh[i], cc2, fma(g[i], rr, cc1));
+            o[j] = q.lo(), o[j + 1] = q.hi();
+          }
+        }
+        store_chunk<T>(p, out, c, o);
       }
     }
   }
 
   // The block's partial sums.
+  const auto& p = part_of;
   const int sums = a.has_bias ? 2 : 1;
-  float* part = a.part + (int64_t)blockIdx.x * sums * cols;
-  if constexpr (kBlock) {
+  float* part = a.part + (int64_t)blockIdx.x * sums * a.cols;
+  if constexpr (B::kGroups == 1) {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int col = (i / VEC * tpr + t) * VEC + i % VEC;
-      if (col < cols) {
-        part[col] = dw[i];
-        if (a.has_bias) part[cols + col] = db[i];
+      const int c = i / VEC, j = i % VEC;
+      if (p.in(c, j)) {
+        part[p.col(c) + j] = i % 2 ? dw[i / 2].hi() : dw[i / 2].lo();
+        if (a.has_bias) part[a.cols + p.col(c) + j] = i % 2 ? db[i / 2].hi() : db[i / 2].lo();
       }
     }
   } else {
     // Every group's in shared memory (over the rings and weights), then added
-    // by column in the groups' order; one sum after the other, which bounds
-    // the room at 4 kThreads E bytes.
+    // by column in the groups' order, one sum after the other.
     float* all = reinterpret_cast<float*>(smem);
     constexpr int kCols = kTpr * E;
     for (int q = 0; q < sums; ++q) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const int col = (i / VEC * kTpr + t) * VEC + i % VEC;
-        all[threadIdx.x / kTpr * kCols + col] = q ? db[i] : dw[i];
+        const Pair s = q ? db[i / 2] : dw[i / 2];
+        all[threadIdx.x / kTpr * kCols + (i / VEC * kTpr + p.t) * VEC + i % VEC] = i % 2 ? s.hi() : s.lo();
       }
       __syncthreads();
-      for (int col = threadIdx.x; col < cols; col += kThreads) {
+      for (int col = threadIdx.x; col < a.cols; col += B::kBlock) {
         float s = 0.f;
-#pragma unroll
-        for (int g = 0; g < groups; ++g) s += all[g * kCols + col];
-        part[q * cols + col] = s;
+#pragma unroll 8
+        for (int g = 0; g < B::kGroups; ++g) s += all[g * kCols + col + p.shift];
+        part[q * a.cols + col] = s;
       }
     }
   }
@@ -523,112 +614,128 @@ norm_finalize_kernel(const float* part, int cols, int sums, int w_bf16, const __
 // ------------------------------------------------------------------ host
 template <int N>
 using Int = std::integral_constant<int, N>;
-// f(elements a lane, lanes a row) for the kernels where a warp or less takes
-// a row: as few lanes as hold it with 8 elements each, then more elements.
-template <typename F>
-void by_lanes(int cols, F f) {
-  if (cols <= 64) f(Int<8>(), Int<8>());
-  else if (cols <= 128) f(Int<8>(), Int<16>());
-  else if (cols <= 256) f(Int<8>(), Int<32>());
-  else if (cols <= 512) f(Int<16>(), Int<32>());
-  else if (cols <= 768) f(Int<24>(), Int<32>());
-  else f(Int<32>(), Int<32>());
-}
-template <typename F>
-void by_weight(int bf16, F f) {
-  if (bf16) f(__nv_bfloat16());
-  else f(float());
-}
-int block_threads(int cols) { return (int)round_up((size_t)ceil_div(cols, kBlockElems), 32); }
-
-template <typename T, int VEC>
-void forward_launch(const NormArgs& a, int sms, cudaStream_t st) {
-  auto grid = [&](int64_t rows_a_block, int64_t blocks_an_sm) {
-    const int64_t n = ceil_div(a.rows, rows_a_block), most = sms * blocks_an_sm;
-    return (unsigned)(n < most ? n : most);
-  };
-  const int threads = block_threads(a.cols);
-  if (a.cols <= kWarpCols)
-    by_lanes(a.cols, [&](auto e, auto lanes) {
-      constexpr int kE = decltype(e)::value, kTpr = decltype(lanes)::value;
-      constexpr auto k = norm_forward_kernel<T, float, VEC, kE, kTpr>;
-      const size_t smem = Rows<T, VEC, kE, kRowSlots<T, kE>>::bytes(kThreads) + 2 * 4 * kE * kTpr;
-      k<<<grid(kThreads / kTpr, resident_blocks<k>(kThreads, smem)), kThreads, smem, st>>>(a);
-    });
-  else if (threads <= kBlockThreads) {
-    const size_t smem = Rows<T, VEC, kBlockElems, kRowSlots<T, kBlockElems>>::bytes(threads);
-    by_weight(a.w_bf16, [&](auto w) {
-      constexpr auto k = norm_forward_kernel<T, decltype(w), VEC, kBlockElems, 0>;
-      k<<<grid(1, resident_blocks<k>(threads, smem)), threads, smem, st>>>(a);
-    });
+// f(elements a thread, threads a row) for rows that reach over `span`
+// elements, false where no kernel holds them.  Few threads with 8 elements
+// each, up to a warp, then more elements (fewer threads have less to exchange),
+// then more warps.  The backward's column sums leave room for 16 elements a
+// thread where several warps have a row.
+template <bool kBackward, typename F>
+bool by_span(int span, F f) {
+  if (span <= 8) return f(Int<8>(), Int<1>());
+  if (span <= 16) return f(Int<8>(), Int<2>());
+  if (span <= 32) return f(Int<8>(), Int<4>());
+  if (span <= 64) return f(Int<8>(), Int<8>());
+  if (span <= 128) return f(Int<8>(), Int<16>());
+  if (span <= 256) return f(Int<8>(), Int<32>());
+  if (span <= 512) return f(Int<16>(), Int<32>());
+  if (span <= 768) return f(Int<24>(), Int<32>());
+  if (span <= 1024) return f(Int<32>(), Int<32>());
+  if constexpr (kBackward) {
+    if (span <= 2048) return f(Int<16>(), Int<128>());
+    if (span <= 4096) return f(Int<16>(), Int<256>());
+    if (span <= 8192) return f(Int<16>(), Int<512>());
   } else {
-    norm_forward_wide_kernel<T, VEC><<<grid(1, 4), kWideThreads, 0, st>>>(a);
+    if (span <= 1536) return f(Int<24>(), Int<64>());
+    if (span <= 2048) return f(Int<32>(), Int<64>());
+    if (span <= 4096) return f(Int<32>(), Int<128>());
+    if (span <= 8192) return f(Int<32>(), Int<256>());
+    if (span <= 12288) return f(Int<32>(), Int<384>());
+  }
+  return false;
+}
+
+template <typename T, int VEC, bool kWhole>
+void forward_launch(const NormArgs& a, int sms, cudaStream_t st) {
+  const bool held = by_span<false>(a.cols + (a.period > 1 ? VEC - 1 : 0), [&](auto e, auto tpr) {
+    constexpr int kE = decltype(e)::value, kTpr = decltype(tpr)::value;
+    using F = Forward<T, VEC, kE, kTpr, kWhole>;
+    constexpr auto k = norm_forward_kernel<T, VEC, kE, kTpr, kWhole>;
+    const int64_t most = (int64_t)sms * resident_blocks<k>(F::kBlock, F::kSmem) / a.period * a.period;
+    int64_t blocks = ceil_div(a.rows, (int64_t)F::kGroups * a.period) * a.period;
+    if (blocks > most) blocks = most < a.period ? a.period : most;
+    k<<<(unsigned)blocks, F::kBlock, F::kSmem, st>>>(a);
+    return true;
+  });
+  if (!held) {
+    const int64_t most = (int64_t)sms * 4;
+    norm_forward_wide_kernel<T, kWhole ? VEC : 1><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
   }
 }
 
 // Blocks of the backward pass, shared out over the workers by their rows: a
-// worker with rows has at least one.
-int block_share(int n_workers, const int64_t* row_begin, int groups, int most, WorkerBlocks* share) {
+// whole number of periods for each, none for one without rows.
+int block_share(int n_workers, const int64_t* row_begin, int rows_a_block, int most, int period, WorkerBlocks* share) {
   const int64_t rows = row_begin[n_workers];
   int n = 0;
   for (int m = 0; m < n_workers; ++m) {
     const int64_t mine = row_begin[m + 1] - row_begin[m];
-    int64_t b = rows ? (int64_t)((double)mine / (double)rows * most) : 0;
-    const int64_t useful = ceil_div(mine, groups);
+    int64_t b = rows ? (int64_t)((double)mine / (double)rows * (most / period)) : 0;
+    const int64_t useful = ceil_div(mine, (int64_t)rows_a_block * period);
     if (b > useful) b = useful;
     if (b < 1 && mine > 0) b = 1;
     share->begin[m] = n;
-    n += (int)b;
+    n += (int)b * period;
   }
   share->begin[n_workers] = n;
   return n;
 }
 
 constexpr int kBwdBlocksPerSm = 8;
-// Of blocks at most: those of every SM, and one more for each worker whose
-// share rounds to none.
-int bwd_max_blocks(int sms, int n_workers) { return sms * kBwdBlocksPerSm + n_workers; }
+// Of blocks at most: those of every SM, and a period (at most 8) more for each
+// worker whose share rounds to none.
+int bwd_max_blocks(int sms, int n_workers) { return sms * kBwdBlocksPerSm + 8 * n_workers; }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool kWhole>
 void backward_launch(const NormArgs& a, const WorkerRows& rows, const int64_t* row_begin, int sms, WorkerBlocks* share,
                      cudaStream_t st) {
-  auto blocks = [&](int rows_a_block, int blocks_an_sm) {
-    return block_share(a.n_workers, row_begin, rows_a_block,
-                       sms * (blocks_an_sm < kBwdBlocksPerSm ? blocks_an_sm : kBwdBlocksPerSm), share);
-  };
-  const int threads = block_threads(a.cols);
   if (!a.rows) return;
-  if (a.cols <= kWarpCols)
-    by_lanes(a.cols, [&](auto e, auto lanes) {
-      constexpr int kE = decltype(e)::value, kTpr = decltype(lanes)::value;
-      constexpr auto k = norm_backward_kernel<T, float, VEC, kE, kTpr>;
-      const size_t rings = 2 * Rows<T, VEC, kE, kRowSlots<T, 2 * kE>>::bytes(kThreads) + 4 * kE * kTpr;
-      const size_t sums = 4 * kThreads * kE, smem = rings > sums ? rings : sums;
-      const int n = blocks(kThreads / kTpr, resident_blocks<k>(kThreads, smem));
-      k<<<n, kThreads, smem, st>>>(a, rows, *share);
-    });
-  else if (threads <= kBlockThreads) {
-    const size_t smem = 2 * Rows<T, VEC, kBlockElems, kRowSlots<T, 2 * kBlockElems>>::bytes(threads);
-    by_weight(a.w_bf16, [&](auto w) {
-      constexpr auto k = norm_backward_kernel<T, decltype(w), VEC, kBlockElems, 0>;
-      const int n = blocks(1, resident_blocks<k>(threads, smem));
-      k<<<n, threads, smem, st>>>(a, rows, *share);
-    });
-  } else {
+  const bool held = by_span<true>(a.cols + (a.period > 1 ? VEC - 1 : 0), [&](auto e, auto tpr) {
+    constexpr int kE = decltype(e)::value, kTpr = decltype(tpr)::value;
+    using B = Backward<T, VEC, kE, kTpr, kWhole>;
+    constexpr auto k = norm_backward_kernel<T, VEC, kE, kTpr, kWhole>;
+    const int resident = resident_blocks<k>(B::kBlock, B::kSmem);
+    const int blocks = block_share(a.n_workers, row_begin, B::kGroups,
+                                   sms * (resident < kBwdBlocksPerSm ? resident : kBwdBlocksPerSm), a.period, share);
+    k<<<blocks, B::kBlock, B::kSmem, st>>>(a, rows, *share);
+    return true;
+  });
+  if (!held) {
     const int64_t most = (int64_t)sms * 4;
-    norm_backward_wide_kernel<T, VEC><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
-    const int n = blocks(64, 1);
-    norm_columns_kernel<T><<<dim3((unsigned)n, (unsigned)ceil_div(a.cols, 32)), 256, 0, st>>>(a, rows, *share);
+    norm_backward_wide_kernel<T, kWhole ? VEC : 1><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
+    const int blocks = block_share(a.n_workers, row_begin, 64, sms, 1, share);
+    norm_columns_kernel<T><<<dim3((unsigned)blocks, (unsigned)ceil_div(a.cols, 32)), 256, 0, st>>>(a, rows, *share);
   }
 }
 
+// How rows are accessed: 16 bytes at a time if every buffer starts on 16 bytes
+// and the buffers' rows start at the same place within 16 bytes, else element
+// by element.
+struct Access {
+  bool wide;
+  int period;
+};
+Access access_of(signmuon_dtype t, int n, const void* const* p, const int64_t* ld) {
+  const int vec = 16 / dtype_bytes(t);
+  for (int i = 0; i < n; ++i)
+    if (!aligned_to(p[i], 16) || ld[i] % vec != ld[0] % vec) return {false, 1};
+  int period = 1;
+  while (ld[0] * period % vec) period *= 2;
+  return {true, period};
+}
+
+// f(type, elements an access, whether rows are whole accesses)
 template <typename F>
-void by_vec(signmuon_dtype t, int vec, F f) {
-  using bf16 = __nv_bfloat16;
-  if (t == SIGNMUON_F32) vec == 4 ? f(float(), std::integral_constant<int, 4>()) : f(float(), std::integral_constant<int, 1>());
-  else if (vec == 8) f(bf16(), std::integral_constant<int, 8>());
-  else if (vec == 2) f(bf16(), std::integral_constant<int, 2>());
-  else f(bf16(), std::integral_constant<int, 1>());
+void by_access(signmuon_dtype t, const Access& access, int cols, F f) {
+  const bool whole = access.period == 1 && cols % (16 / dtype_bytes(t)) == 0;
+  if (t == SIGNMUON_F32) {
+    if (!access.wide) f(float(), Int<1>(), std::true_type());
+    else if (whole) f(float(), Int<4>(), std::true_type());
+    else f(float(), Int<4>(), std::false_type());
+  } else {
+    if (!access.wide) f(__nv_bfloat16(), Int<1>(), std::true_type());
+    else if (whole) f(__nv_bfloat16(), Int<8>(), std::true_type());
+    else f(__nv_bfloat16(), Int<8>(), std::false_type());
+  }
 }
 
 }  // namespace
@@ -648,14 +755,15 @@ signmuon_status signmuon_layer_norm_forward(int64_t rows, int32_t cols, signmuon
       !aligned_to(mean, 4) || !aligned_to(rstd, 4))
     return SIGNMUON_ERR_ALIGNMENT;
   if (!rows) return SIGNMUON_OK;
-  int vec = vec_width(x_dtype, cols);
-  vec = vec_narrow(vec, x_dtype, x, ld_x);
-  vec = vec_narrow(vec, x_dtype, y, ld_y);
+  const void* const bufs[2] = {x, y};
+  const int64_t lds[2] = {ld_x, ld_y};
+  const Access access = access_of(x_dtype, 2, bufs, lds);
   NormArgs a = {};
+  a.period = access.period;
   a.rows = rows, a.cols = cols, a.x = x, a.out = y, a.ld_x = ld_x, a.ld_out = ld_y, a.w = weight, a.b = bias;
   a.w_bf16 = w_dtype == SIGNMUON_BF16, a.eps = eps, a.mean = mean, a.rstd = rstd;
-  by_vec(x_dtype, vec, [&](auto t, auto v) {
-    forward_launch<decltype(t), decltype(v)::value>(a, current_sms(), static_cast<cudaStream_t>(stream));
+  by_access(x_dtype, access, cols, [&](auto t, auto v, auto whole) {
+    forward_launch<decltype(t), decltype(v)::value, decltype(whole)::value>(a, current_sms(), static_cast<cudaStream_t>(stream));
   });
   return cuda_status(cudaGetLastError());
 }
@@ -694,11 +802,11 @@ signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const 
   const signmuon_status st =
       check_ws(workspace, ws_bytes, signmuon_layer_norm_backward_workspace_bytes(cols, n_workers, row_begin));
   if (st) return st;
-  int vec = vec_width(x_dtype, cols);
-  vec = vec_narrow(vec, x_dtype, x, ld_x);
-  vec = vec_narrow(vec, x_dtype, dy, ld_dy);
-  vec = vec_narrow(vec, x_dtype, dx, ld_dx);
+  const void* const bufs[3] = {x, dy, dx};
+  const int64_t lds[3] = {ld_x, ld_dy, ld_dx};
+  const Access access = access_of(x_dtype, 3, bufs, lds);
   NormArgs a = {};
+  a.period = access.period;
   a.rows = n, a.cols = cols, a.x = x, a.dy = dy, a.out = dx, a.ld_x = ld_x, a.ld_dy = ld_dy, a.ld_out = ld_dx;
   a.w = weight, a.w_bf16 = w_dtype == SIGNMUON_BF16, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeaderBytes);
@@ -707,8 +815,8 @@ signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const 
   for (int m = 0; m <= n_workers; ++m) rows.begin[m] = row_begin[m];
   WorkerBlocks share = {};
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  by_vec(x_dtype, vec, [&](auto t, auto v) {
-    backward_launch<decltype(t), decltype(v)::value>(a, rows, row_begin, current_sms(), &share, cs);
+  by_access(x_dtype, access, cols, [&](auto t, auto v, auto whole) {
+    backward_launch<decltype(t), decltype(v)::value, decltype(whole)::value>(a, rows, row_begin, current_sms(), &share, cs);
   });
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);

@@ -77,13 +77,40 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   *reinterpret_cast<typename RawVec<T, VEC>::type*>(p) = r;
 }
 
-// Asynchronous copies of 4 or 16 bytes to shared memory, seen by the thread
+// Two fp32 in a register pair, and arithmetic on both with one instruction.
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ Pair() {}
+  __device__ __forceinline__ Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ float lo() const { return __uint_as_float((uint32_t)v); }
+  __device__ __forceinline__ float hi() const { return __uint_as_float((uint32_t)(v >> 32)); }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// Asynchronous copies of 4 or 16 bytes to shared memory, of which only the
+// first `valid` bytes are read and the others are zero; seen by the thread
 // that issued them once its group is waited for.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* smem, const void* global) {
+template <int BYTES, bool kAll>
+__device__ __forceinline__ void copy_async(void* smem, const void* global, int valid) {
   const uint32_t dst = (uint32_t)__cvta_generic_to_shared(smem);
-  if constexpr (BYTES == 16)
+  if constexpr (BYTES == 16 && kAll)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(global) : "memory");
+  else if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(global), "r"(valid) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(global), "n"(BYTES) : "memory");
 }
