@@ -14,6 +14,9 @@
 //   2. rows      the logits: running maximum and sum, the row's loss, and the
 //                gradient;
 //   3. workers   the losses of each worker's rows, added in a fixed order.
+// The second one reads the logits and writes the gradient, each once, and is
+// bound by that: a block (for long rows a cluster of blocks) holds its row in
+// shared memory from the pass that sums to the pass that writes.
 #include <cmath>
 
 #include "layers.cuh"
@@ -24,7 +27,15 @@ namespace {
 
 constexpr int kMaxTop = 1024;
 constexpr int kTeacherWarps = 4;
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 512;           // of a block that reads its row twice
+constexpr int kHeldThreads = 384;          // of a block that holds its row, at most
+constexpr int kBatch = 3;                  // chunks a thread copies as one group
+constexpr int kDepth = 5;                  // groups under way where a row is not held
+constexpr int kMaxCluster = 8;
+constexpr int kSplitThreads = 256;         // ... of a block that holds a part of it, at most
+constexpr int kRowBytes = 110 * 1024;      // of a row that two blocks an SM can hold each
+constexpr int kSliceBytes = 73 * 1024;     // of its parts, that three blocks an SM can hold
+constexpr int kSmSmem = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A teacher's entry: its id (-1: none) and the probability it holds.
@@ -47,21 +58,36 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // ---------------------------------------------------------------- teacher
 __global__ void __launch_bounds__(kTeacherWarps * 32)
 teacher_kernel(int64_t rows, int top, const void* __restrict__ ids, int wide, const void* __restrict__ logits, int bf16,
-               int32_t vocab, float inv_t, Entry* __restrict__ entries, float* __restrict__ plogp, uint8_t* __restrict__ counts) {
-  extern __shared__ Entry s_entries[];
+               int32_t vocab, float inv_t, int log_slots, Entry* __restrict__ entries, float* __restrict__ plogp, uint8_t* __restrict__ counts) {
+  extern __shared__ Entry s_entries[];  // each warp: its entries, then its table of ids
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int64_t row = (int64_t)blockIdx.x * kTeacherWarps + warp;
   if (row >= rows) return;
   Entry* mine = s_entries + warp * top;
+  int32_t* table = reinterpret_cast<int32_t*>(s_entries + kTeacherWarps * top) + (warp << log_slots);
+  for (int i = lane; i < 1 << log_slots; i += 32) table[i] = -1;
+  __syncwarp();
   float top_u = -INFINITY;
-  bool any = false, bad = false;
+  bool any = false, bad = false, twice = false;
+#pragma unroll 4
   for (int k = lane; k < top; k += 32) {
     const int64_t id = load_id(ids, row * top + k, wide);
     const float u = load_elem(logits, row * top + k, bf16);
-    const bool in = id >= 0 && id < vocab && u != -INFINITY;
-    mine[k] = {in ? (int32_t)id : -1, u};
-    if (in) top_u = fmaxf(top_u, u), any = true, bad |= u != u;
+    mine[k] = {id >= 0 && id < vocab && u != -INFINITY ? (int32_t)id : -1, u};
   }
+  for (int k = lane; k < top; k += 32) {
+    const Entry e = mine[k];
+    if (e.id < 0) continue;
+    top_u = fmaxf(top_u, e.p), any = true, bad |= e.p != e.p;
+    // Ids in a hash table of at least twice as many slots, to see whether one
+    // comes twice.
+    for (uint32_t at = (uint32_t)e.id * 2654435769u >> (32 - log_slots);; at = (at + 1) & ((1u << log_slots) - 1)) {
+      const int32_t seen = atomicCAS(&table[at], -1, e.id);
+      twice |= seen == e.id;
+      if (seen == -1 || seen == e.id) break;
+    }
+  }
+  twice = __any_sync(0xffffffffu, twice);
   any = __any_sync(0xffffffffu, any);
   // fmaxf drops a NaN: one among the entries makes the row NaN.
   top_u = __any_sync(0xffffffffu, bad) ? NAN : warp_max(top_u);
@@ -82,7 +108,9 @@ teacher_kernel(int64_t rows, int top, const void* __restrict__ ids, int wide, co
   // The first entry of an id holds all of the id's.
   for (int k = lane; k < top; k += 32) {
     Entry e = mine[k];
-    if (e.id >= 0) {
+    if (e.id >= 0 && !twice) {
+      if (e.p == 0.f) e.id = -1;
+    } else if (e.id >= 0) {
       float p = 0.f;
       bool first = true;
       for (int j = 0; j < top; ++j) {
@@ -115,36 +143,423 @@ struct RowArgs {
   float t, inv_t, grad_scale;
 };
 
-// Running maximum and sum of 2^((z - max) c).
+// A sum of 2^(c z) as s 2^e, c = log2(e) / T and e a whole number, at least c
+// times the largest z so far.  c z - e is one fused multiply-add, rounded once
+// and only to the size of the difference, and changing e multiplies s by a
+// power of two.  An empty sum has e = -inf and s = 0.
 struct Soft {
-  float m, s;
+  float e, s;
 };
-__device__ __forceinline__ Soft soft_join(Soft a, Soft b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  // An empty part has m = -inf and s = 0 and drops out.
-  const float s = (a.m == -INFINITY ? a.s : a.s * exp2_fast((a.m - m) * c)) + (b.m == -INFINITY ? b.s : b.s * exp2_fast((b.m - m) * c));
-  return {m, s};
-}
-template <int N>
-__device__ __forceinline__ void soft_add(Soft& a, const float (&v)[N], float c) {
-  float m = v[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
-  if (m > a.m) {
-    a.s = a.m == -INFINITY ? a.s : a.s * exp2_fast((a.m - m) * c);
-    a.m = m;
+__device__ __forceinline__ float soft_ref(float e) { return e == -INFINITY ? 0.f : -e; }  // added to c z
+__device__ __forceinline__ void soft_raise(Soft& a, float top, float c) {
+  const float e = ceilf(top * c);
+  if (e > a.e) {
+    a.s *= a.e == -INFINITY ? 0.f : exp2_fast(a.e - e);
+    a.e = e;
   }
-  // While nothing finite has come (m is -inf), differences are NaN unless
-  // they are taken to 0; then every term is 2^-inf = 0.
-  const float base = a.m == -INFINITY ? 0.f : a.m;
-  float s = 0.f;
+}
+__device__ __forceinline__ Soft soft_join(Soft a, Soft b) {
+  const float e = fmaxf(a.e, b.e);
+  return {e, (a.e == -INFINITY ? a.s : a.s * exp2_fast(a.e - e)) + (b.e == -INFINITY ? b.s : b.s * exp2_fast(b.e - e))};
+}
+__device__ __forceinline__ Soft warp_join(Soft a) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) s += exp2_fast((v[i] - base) * c);
-  a.s += s;
+  for (int o = 16; o; o >>= 1)
+    a = soft_join(a, {__shfl_xor_sync(0xffffffffu, a.e, o), __shfl_xor_sync(0xffffffffu, a.s, o)});
+  return a;
+}
+// log q of a logit.
+__device__ __forceinline__ float soft_log(Soft a, float z, float c) {
+  return (fmaf(z, c, -a.e) - log2f(a.s)) * 0.6931471805599453f;
 }
 
-// Rows of any alignment: elements before the first and after the last whole
-// 16 bytes are taken one at a time.
+// --------------------------------------------------- rows in shared memory
+// A row is taken in chunks of 16 bytes that start on 16 bytes; its first chunk
+// may begin before it (in the row before), its last is filled up with what is
+// masked.  The chunks are split over the blocks of a cluster, and a block's
+// over its threads, which each copy, read and write their own: no barrier but
+// those of the sums.  For the gradient a block holds its part of the row; as
+// soon as a thread has written the gradient of a batch of kBatch chunks it
+// starts the copies of the next row's batch into the same place, which go on
+// while the sums are joined and the other block of the SM computes.  For the
+// losses alone a block holds the kDepth batches that come next.
+//
+// With two exponentials an element the kernel is nearly bound by instructions
+// as well (8.2 an element without any bookkeeping), so the batches that every
+// thread has whole run without tests, at addresses that differ by constants
+// (kThreads is the block's size where it is not 0), and what is left, and the
+// ends of rows, chunk by chunk.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<float> {
+  static constexpr int kVec = 4;
+  float4 r;
+  __device__ __forceinline__ void clear() { r = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+  __device__ __forceinline__ void get(Pair (&v)[2]) const { v[0] = Pair(r.x, r.y), v[1] = Pair(r.z, r.w); }
+  __device__ __forceinline__ float max() const { return fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)); }
+  // Keeps elements [lo, hi), the others are -inf.  (Not inlined: it would be
+  // run under a false predicate by every chunk.)
+  __device__ __noinline__ static float4 mask(float4 r, int lo, int hi) {
+    r.x = 0 >= lo && 0 < hi ? r.x : -INFINITY, r.y = 1 >= lo && 1 < hi ? r.y : -INFINITY;
+    r.z = 2 >= lo && 2 < hi ? r.z : -INFINITY, r.w = 3 >= lo && 3 < hi ? r.w : -INFINITY;
+    return r;
+  }
+};
+template <>
+struct Chunk<__nv_bfloat16> {
+  static constexpr int kVec = 8;
+  uint4 r;
+  __device__ __forceinline__ void clear() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+  __device__ __forceinline__ void get(Pair (&v)[4]) const {
+    v[0] = Pair(bf16_lo(r.x), bf16_hi(r.x)), v[1] = Pair(bf16_lo(r.y), bf16_hi(r.y));
+    v[2] = Pair(bf16_lo(r.z), bf16_hi(r.z)), v[3] = Pair(bf16_lo(r.w), bf16_hi(r.w));
+  }
+  __device__ __forceinline__ static __nv_bfloat162 pair(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
+  __device__ __forceinline__ float max() const {
+    const float2 m = __bfloat1622float2(__hmax2(__hmax2(pair(r.x), pair(r.y)), __hmax2(pair(r.z), pair(r.w))));
+    return fmaxf(m.x, m.y);
+  }
+  __device__ __noinline__ static uint4 mask(uint4 r, int lo, int hi) {
+    uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (2 * i < lo || 2 * i >= hi) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+      if (2 * i + 1 < lo || 2 * i + 1 >= hi) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A thread's chunks of a row: q = 0 .. n - 1 at element q * stride of `at`,
+// which may lie before the row (then the first chunk's first elements do).
+struct Mine {
+  int64_t at;     // element of the buffer where chunk 0 starts
+  int col;        // its column
+  int n;
+  uint32_t ends;  // batches with an end of the row in this warp
+};
+
+// The rows first, first + step, ... that count.  A warp looks up 32 of them at
+// a time.
+struct RowWalk {
+  int64_t base, step;  // row of bit 0
+  uint32_t counts, rows;  // rows of the 32 that count, and that are there, from bit `at` on
+  __device__ __forceinline__ RowWalk(const RowArgs& a, int64_t first, int64_t step) : base(first), step(step) { look(a); }
+  __device__ __forceinline__ void look(const RowArgs& a) {
+    const int64_t r = base + (threadIdx.x & 31) * step;
+    rows = __ballot_sync(0xffffffffu, r < a.rows);
+    counts = __ballot_sync(0xffffffffu, r < a.rows && a.counts[r]);
+  }
+  // The next row that counts (a.rows: none); skip(row) for those before it
+  // that do not.
+  template <typename F>
+  __device__ __forceinline__ int64_t next(const RowArgs& a, F skip) {
+    while (rows) {
+      const int at = __ffs(rows) - 1;
+      const uint32_t bit = 1u << at;
+      const bool hit = counts & bit;
+      const int64_t row = base + at * step;
+      rows &= ~bit;
+      if (!rows) {
+        base += 32 * step;
+        look(a);
+      }
+      if (hit) return row;
+      skip(row);
+    }
+    return a.rows;
+  }
+};
+
+template <typename T, bool kGrad, int kThreads>
+__global__ void __launch_bounds__(kHeldThreads, 2)
+held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, int slice) {
+  constexpr int kVec = Chunk<T>::kVec;
+  // The block's chunks (for the losses kDepth batches), and the entries' logits.
+  extern __shared__ __align__(16) uint8_t held[];
+  __shared__ Soft s_soft[2][kHeldThreads / 32], s_block[2][kMaxCluster];
+  __shared__ float s_cross[kHeldThreads / 32];
+  __shared__ int s_n;
+  const int threads = kThreads ? kThreads : blockDim.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = threads / 32;
+  // Whole batches of every thread, and one more of what is left.
+  const int full = slice / (kBatch * threads), batches = full + 1;
+  Chunk<T>* const mine = reinterpret_cast<Chunk<T>*>(held) + threadIdx.x;
+  float* const entry_z = reinterpret_cast<float*>(held + (size_t)(kGrad ? slice : kDepth * kBatch * threads) * 16);
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  const int64_t step = gridDim.x / ranks;
+  const int first = rank * slice, stride = threads * kVec;
+  const float c = a.inv_t * kLog2e;
+  const Pair cc(c, c);
+  const T* const z_all = static_cast<const T*>(a.z);
+  T* const dz_all = static_cast<T*>(a.dz);
+
+  auto shift_of = [&](int64_t row) { return (int)(row * a.ld_z % kVec); };
+  auto mine_of = [&](int64_t row) {
+    const int shift = shift_of(row), chunk = first + threadIdx.x;
+    const int end = min(first + slice, (a.vocab + shift + kVec - 1) / kVec);  // the row's chunks, and this block's
+    Mine m;
+    m.col = chunk * kVec - shift;
+    m.at = row * a.ld_z + m.col;
+    m.n = chunk < end ? (end - chunk + threads - 1) / threads : 0;
+    // The whole batches of this warp that are not whole in this row: with its
+    // first chunk, or its last, or after it.
+    uint32_t ends = m.n > 0 && m.col < 0 ? 1u : 0u;
+    if (m.n > 0 && m.col + (m.n - 1) * stride + kVec > a.vocab) ends |= 1u << min((m.n - 1) / kBatch, 31);
+    if (m.n < full * kBatch) ends |= ~0u << min(m.n / kBatch, 31);
+    m.ends = __reduce_or_sync(0xffffffffu, ends);
+    return m;
+  };
+  auto plain = [&](const Mine& m, int b) { return b < full && !(m.ends >> min(b, 31) & 1); };
+  auto whole = [&](int col) { return col >= 0 && col + kVec <= a.vocab; };
+  // Copies of a batch (what a chunk has after the row's end is not read).
+  auto fetch = [&](const Mine& m, int b, int slot) {
+    Chunk<T>* to = mine + slot * kBatch * threads;
+    const T* from = z_all + m.at + b * kBatch * stride;
+    if (plain(m, b)) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) copy_async<16, true>(to + i * threads, from + i * stride, 16);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kBatch && b * kBatch + i < m.n; ++i)
+        copy_async<16, false>(to + i * threads, from + i * stride,
+                              min(a.vocab - (m.col + (b * kBatch + i) * stride), kVec) * (int)sizeof(T));
+      __syncwarp();
+    }
+    copy_commit();
+  };
+  auto zero_row = [&](int64_t row) {
+    if (rank == 0 && threadIdx.x == 0) a.row_loss[row] = 0.f;
+    if (kGrad) {
+      const Mine m = mine_of(row);
+      T* dz = dz_all + row * a.ld_dz;
+      for (int q = 0; q < m.n; ++q) {
+        const int col = m.col + q * stride;
+        if (col >= 0 && col + kVec <= a.vocab) {
+          __stcs(reinterpret_cast<uint4*>(dz + col), make_uint4(0, 0, 0, 0));
+        } else {
+          for (int i = max(col, 0); i < min(col + kVec, a.vocab); ++i) store_elem(dz, i, sizeof(T) == 2, 0.f);
+        }
+      }
+    }
+  };
+
+  if (ranks > 1) cluster_sync();  // all blocks run before one writes to another
+  // Rows of this block that count, two walks over them: `far` is the row whose
+  // batches are fetched next, `row` the one at work.  The first one also does
+  // what there is to do for the rows that do not count.
+  RowWalk far_walk(a, blockIdx.x / ranks, step), walk = far_walk;
+  int64_t far = far_walk.next(a, zero_row), row = walk.next(a, [](int64_t) {});
+  Mine now = row < a.rows ? mine_of(row) : Mine{0, 0, 0, ~0u}, fetched = now;
+  int ahead = 0;
+  auto fetch_next = [&](int slot) {
+    fetch(fetched, ahead, slot);
+    if (++ahead == batches) {
+      ahead = 0;
+      far = far_walk.next(a, zero_row);
+      fetched = far < a.rows ? mine_of(far) : Mine{0, 0, 0, ~0u};
+    }
+  };
+  for (int b = 0; b < (kGrad ? batches : kDepth); ++b) fetch_next(b);
+  int worker = -1, turn = 0, slot = 0;
+  float scale = 0.f;
+  // Each thread's first entry, a row ahead, so that nothing waits for it.
+  const Entry none = {-1, 0.f};
+  Entry entry_next = row < a.rows && (int)threadIdx.x < a.top ? a.entries[row * a.top + threadIdx.x] : none;
+  while (row < a.rows) {
+    const int64_t row_next = walk.next(a, [](int64_t) {});
+    // The entries' logits, before the gradient may take their place.
+    const Entry* entries = a.entries + row * a.top;
+    const Entry entry = entry_next;
+    float logit = 0.f;
+    if (entry.id >= 0) logit = load_elem(a.z, row * a.ld_z + entry.id, sizeof(T) == 2);
+    entry_next = row_next < a.rows && (int)threadIdx.x < a.top ? a.entries[row_next * a.top + threadIdx.x] : none;
+    for (int k = threadIdx.x + threads; k < a.top; k += threads)
+      if (entries[k].id >= 0) entry_z[k] = load_elem(a.z, row * a.ld_z + entries[k].id, sizeof(T) == 2);
+    const float plogp = threadIdx.x == 0 ? a.plogp[row] : 0.f;
+
+    Soft soft = {-INFINITY, 0.f};
+    for (int b = 0; b < batches; ++b) {
+      // What may be on its way still: the batches after this one, for the
+      // losses the kDepth - 1 that follow.
+      if constexpr (kGrad) {
+        const int out = full - b;
+        if (out >= 3) copy_wait<3>();
+        else if (out == 2) copy_wait<2>();
+        else if (out == 1) copy_wait<1>();
+        else copy_wait<0>();
+      } else {
+        copy_wait<kDepth - 1>();
+      }
+      const Chunk<T>* from = mine + (kGrad ? b : slot) * kBatch * threads;
+      if (plain(now, b)) {
+        Chunk<T> x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) x[i] = from[i * threads];
+        float top = x[0].max();
+#pragma unroll
+        for (int i = 1; i < kBatch; ++i) top = fmaxf(top, x[i].max());
+        soft_raise(soft, top, c);
+        const Pair ref(soft_ref(soft.e), soft_ref(soft.e));
+        Pair sum(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          Pair v[kVec / 2];
+          x[i].get(v);
+#pragma unroll
+          for (int q = 0; q < kVec / 2; ++q) {
+            const Pair e = fma(v[q], cc, ref);
+            sum = sum + Pair(exp2_fast(e.lo()), exp2_fast(e.hi()));
+          }
+        }
+        soft.s += sum.lo() + sum.hi();
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kBatch && b * kBatch + i < now.n; ++i) {
+          const int col = now.col + (b * kBatch + i) * stride;
+          Chunk<T> x = from[i * threads];
+          if (!whole(col)) x.r = Chunk<T>::mask(x.r, -col, a.vocab - col);
+          soft_raise(soft, x.max(), c);
+          const float ref = soft_ref(soft.e);
+          Pair v[kVec / 2], sum(0.f, 0.f);
+          x.get(v);
+#pragma unroll
+          for (int q = 0; q < kVec / 2; ++q) {
+            const Pair e = fma(v[q], cc, Pair(ref, ref));
+            sum = sum + Pair(exp2_fast(e.lo()), exp2_fast(e.hi()));
+          }
+          soft.s += sum.lo() + sum.hi();
+        }
+      }
+      if constexpr (!kGrad) {
+        __syncwarp();
+        fetch_next(slot);
+        slot = slot == kDepth - 1 ? 0 : slot + 1;
+      }
+    }
+    __syncwarp();
+    soft = warp_join(soft);
+    if (lane == 0) s_soft[turn][warp] = soft;
+    __syncthreads();
+    // Every warp joins the warps' parts, in the same order of lanes.
+    soft = warp_join(lane < warps ? s_soft[turn][lane] : Soft{-INFINITY, 0.f});
+    if (ranks > 1) {
+      if (threadIdx.x < ranks) {
+        uint32_t at;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(at)
+            : "r"((uint32_t)__cvta_generic_to_shared(&s_block[turn][rank])), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.f32 [%0], %1;\n\tst.shared::cluster.f32 [%0+4], %2;" ::"r"(at), "f"(soft.e), "f"(soft.s)
+                     : "memory");
+      }
+      cluster_sync();
+      soft = s_block[turn][0];
+      for (uint32_t i = 1; i < ranks; ++i) soft = soft_join(soft, s_block[turn][i]);
+    }
+
+    // Loss: sum p log q of the entries, a warp's part each.
+    float cross = entry.id >= 0 ? entry.p * soft_log(soft, logit, c) : 0.f;
+    for (int k = threadIdx.x + threads; k < a.top; k += threads)
+      if (entries[k].id >= 0) cross = fmaf(entries[k].p, soft_log(soft, entry_z[k], c), cross);
+    cross = warp_sum(cross);
+    if (lane == 0) s_cross[warp] = cross;
+    if constexpr (kGrad) {
+      if (worker < 0 || workers.begin[worker + 1] <= row) {
+        // The rows that count of this row's worker.
+        while (workers.begin[++worker + 1] <= row) {}
+        int n = 0;
+        for (int64_t i = workers.begin[worker] + threadIdx.x; i < workers.begin[worker + 1]; i += threads) n += a.counts[i];
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (threadIdx.x == 0) s_n = 0;
+        __syncthreads();
+        if (lane == 0) atomicAdd(&s_n, n);
+        __syncthreads();
+        scale = a.grad_scale * a.t / (float)s_n;
+      }
+      const float qs = scale / soft.s;
+      const Pair ref(soft_ref(soft.e), soft_ref(soft.e)), qq(qs, qs);
+      T* dz = dz_all + row * a.ld_dz + now.col;
+      auto gradient = [&](const Chunk<T>& x, float (&o)[kVec]) {
+        Pair v[kVec / 2];
+        x.get(v);
+#pragma unroll
+        for (int q = 0; q < kVec / 2; ++q) {
+          const Pair e = fma(v[q], cc, ref), g = Pair(exp2_fast(e.lo()), exp2_fast(e.hi())) * qq;
+          o[2 * q] = g.lo(), o[2 * q + 1] = g.hi();
+        }
+      };
+      for (int b = 0; b < batches; ++b, dz += kBatch * stride) {
+        const Chunk<T>* from = mine + b * kBatch * threads;
+        if (plain(now, b)) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            float o[kVec];
+            gradient(from[i * threads], o);
+            store_stream<T, kVec>(dz + i * stride, o);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kBatch && b * kBatch + i < now.n; ++i) {
+            const int col = now.col + (b * kBatch + i) * stride;
+            float o[kVec];
+            gradient(from[i * threads], o);
+            if (whole(col)) {
+              store_stream<T, kVec>(dz + i * stride, o);
+            } else {
+#pragma unroll
+              for (int q = 0; q < kVec; ++q)
+                if (col + q >= 0 && col + q < a.vocab) store_elem(dz, i * stride + q, sizeof(T) == 2, o[q]);
+            }
+          }
+        }
+        __syncwarp();
+        fetch_next(b);
+      }
+      __syncthreads();
+      // The entries' elements of this block's part of the row.
+      const int shift = shift_of(row);
+      auto fix = [&](Entry e, float z) {
+        const int at = e.id >= 0 ? (e.id + shift) / kVec - first : -1;
+        if (at >= 0 && at < slice)
+          store_elem(dz_all, row * a.ld_dz + e.id, sizeof(T) == 2, exp2_fast(fmaf(z, c, soft_ref(soft.e))) * qs - e.p * scale);
+      };
+      fix(entry, logit);
+      for (int k = threadIdx.x + threads; k < a.top; k += threads) fix(entries[k], entry_z[k]);
+    } else {
+      __syncthreads();
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+      float x = 0.f;
+      for (int w = 0; w < warps; ++w) x += s_cross[w];
+      a.row_loss[row] = a.t * a.t * (plogp - x);
+    }
+    row = row_next;
+    now = row < a.rows ? mine_of(row) : Mine{0, 0, 0, ~0u};
+    turn ^= 1;
+  }
+  if (ranks > 1) cluster_sync();
+}
+
+// ------------------------------------------------------- rows of any address
+// Where buffers do not start on 16 bytes, logits and gradient lie differently
+// within them, or a row is too long for a cluster's shared memory: the second
+// pass reads the row again.  Elements before the first and after the last
+// whole 16 bytes are taken one at a time.
 template <typename T>
 struct RowSpan {
   static constexpr int kVec = 16 / sizeof(T);
@@ -175,34 +590,38 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
     }
     const RowSpan<T> span(z, n);
     Soft soft = {-INFINITY, 0.f};
+    auto add = [&](const auto& v) {
+      float top = v[0];
+      for (float x : v) top = fmaxf(top, x);
+      soft_raise(soft, top, c);
+      for (float x : v) soft.s += exp2_fast(fmaf(x, c, soft_ref(soft.e)));
+    };
     for (int i = threadIdx.x; i < span.head + (n - span.body_end); i += kRowThreads) {
-      float v[1] = {load_elem(z, i < span.head ? i : i - span.head + span.body_end, sizeof(T) == 2)};
-      soft_add(soft, v, c);
+      const float v[1] = {load_elem(z, i < span.head ? i : i - span.head + span.body_end, sizeof(T) == 2)};
+      add(v);
     }
-#pragma unroll 4
+#pragma unroll 2
     for (int i = span.head + threadIdx.x * kVec; i < span.body_end; i += kRowThreads * kVec) {
       float v[kVec];
       unpack(*reinterpret_cast<const typename RawVec<T, kVec>::type*>(z + i), v);
-      soft_add(soft, v, c);
+      add(v);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-      soft = soft_join(soft, {__shfl_xor_sync(0xffffffffu, soft.m, o), __shfl_xor_sync(0xffffffffu, soft.s, o)}, c);
+    soft = warp_join(soft);
     __syncthreads();  // the row before is done with the shared values
     if (lane == 0) s_soft[warp] = soft;
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
     soft = s_soft[0];
-    for (int i = 1; i < kRowThreads / 32; ++i) soft = soft_join(soft, s_soft[i], c);
+    for (int i = 1; i < kRowThreads / 32; ++i) soft = soft_join(soft, s_soft[i]);
     const Entry* entries = a.entries + row * a.top;
     if (warp == 0) {
       float x = 0.f;
       for (int k = lane; k < a.top; k += 32) {
         const Entry e = entries[k];
-        if (e.id >= 0) x = fmaf(e.p, (load_elem(z, e.id, sizeof(T) == 2) - soft.m) * a.inv_t, x);
+        if (e.id >= 0) x = fmaf(e.p, soft_log(soft, load_elem(z, e.id, sizeof(T) == 2), c), x);
       }
       x = warp_sum(x);
-      if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - x + logf(soft.s));
+      if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - x);
     }
     if (!dz) continue;
     // The rows of this worker that count.
@@ -213,31 +632,31 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
     cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) atomicAdd(&s_n, cnt);
     __syncthreads();
-    const float scale = a.grad_scale * a.t / (float)s_n, qs = scale / soft.s;
+    const float scale = a.grad_scale * a.t / (float)s_n, qs = scale / soft.s, ref = soft_ref(soft.e);
     // Entries' logits are read before the gradient may overwrite them.
     float fix[kMaxTop / kRowThreads];
     for (int i = 0, k = threadIdx.x; k < a.top; ++i, k += kRowThreads) {
       const Entry e = entries[k];
-      if (e.id >= 0) fix[i] = exp2_fast((load_elem(z, e.id, sizeof(T) == 2) - soft.m) * c) * qs - e.p * scale;
+      if (e.id >= 0) fix[i] = exp2_fast(fmaf(load_elem(z, e.id, sizeof(T) == 2), c, ref)) * qs - e.p * scale;
     }
     __syncthreads();
     const RowSpan<T> out(dz, n);
     if (out.head == span.head) {
       for (int i = threadIdx.x; i < span.head + (n - span.body_end); i += kRowThreads) {
         const int at = i < span.head ? i : i - span.head + span.body_end;
-        store_elem(dz, at, sizeof(T) == 2, exp2_fast((load_elem(z, at, sizeof(T) == 2) - soft.m) * c) * qs);
+        store_elem(dz, at, sizeof(T) == 2, exp2_fast(fmaf(load_elem(z, at, sizeof(T) == 2), c, ref)) * qs);
       }
 #pragma unroll 4
       for (int i = span.head + threadIdx.x * kVec; i < span.body_end; i += kRowThreads * kVec) {
         float v[kVec];
         unpack(*reinterpret_cast<const typename RawVec<T, kVec>::type*>(z + i), v);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = exp2_fast((v[j] - soft.m) * c) * qs;
+        for (int j = 0; j < kVec; ++j) v[j] = exp2_fast(fmaf(v[j], c, ref)) * qs;
         store_stream<T, kVec>(dz + i, v);
       }
     } else {
       for (int i = threadIdx.x; i < n; i += kRowThreads)
-        store_elem(dz, i, sizeof(T) == 2, exp2_fast((load_elem(z, i, sizeof(T) == 2) - soft.m) * c) * qs);
+        store_elem(dz, i, sizeof(T) == 2, exp2_fast(fmaf(load_elem(z, i, sizeof(T) == 2), c, ref)) * qs);
     }
     __syncthreads();
     for (int i = 0, k = threadIdx.x; k < a.top; ++i, k += kRowThreads) {
@@ -265,6 +684,85 @@ worker_loss_kernel(const float* __restrict__ row_loss, const uint8_t* __restrict
     for (int i = 1; i < 8; ++i) sum += s_sum[i], n += s_n[i];
     loss[m] = (float)(sum / (double)(n > 0 ? n : 1));
   }
+}
+
+// Clusters of this launch that the device holds (`guess` if it cannot say),
+// kept for the last configuration asked for.
+template <auto K>
+int resident_clusters(cudaLaunchConfig_t cfg, int guess) {
+  struct Known {
+    int dev = -1, ranks = 0, threads = 0, n = 0;
+    size_t smem = 0;
+  };
+  static thread_local Known known;
+  const int dev = current_device(), ranks = (int)cfg.attrs[0].val.clusterDim.x, threads = (int)cfg.blockDim.x;
+  if (known.dev != dev || known.ranks != ranks || known.threads != threads || known.smem != cfg.dynamicSmemBytes) {
+    cfg.gridDim = dim3((unsigned)ranks);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, K, &cfg) != cudaSuccess || n < 1) n = guess < 1 ? 1 : guess;
+    known.dev = dev, known.ranks = ranks, known.threads = threads, known.smem = cfg.dynamicSmemBytes, known.n = n;
+  }
+  return known.n;
+}
+
+// Launches the pass over the logits.
+template <typename T>
+void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
+  constexpr int kVec = Chunk<T>::kVec;
+  const int sms = current_sms();
+  // For the gradient a block holds a row, if two blocks an SM can, else the
+  // blocks of a cluster do, three an SM; more blocks, also for the losses, where
+  // rows are few.  (8192 rows of 50000 bf16: 336 us by blocks of 384 threads,
+  // 359 of 256, 393 of 512, 377 split in two; 513 rows of 131101 fp32: 120 us
+  // with three blocks an SM, 140 with two.)
+  const int shift = a.ld_z % kVec ? kVec - 1 : 0;
+  const int64_t chunks = ((int64_t)a.vocab + shift + kVec - 1) / kVec;
+  int ranks = 1, threads = 0;
+  int64_t slice = 0, smem = 0;
+  for (;; ranks *= 2) {
+    const int most = ranks > 1 ? kSplitThreads : kHeldThreads;
+    slice = ceil_div(chunks, ranks);
+    threads = (int)round_up((size_t)ceil_div(slice, kBatch), 32);
+    if (threads > most) threads = most;
+    smem = (a.dz ? slice : (int64_t)kDepth * kBatch * threads) * 16 + (int64_t)a.top * 4;
+    if (ranks == kMaxCluster || !(smem > (ranks > 1 ? kSliceBytes : kRowBytes) ||
+                                  (a.rows * ranks * 2 <= sms && chunks >= 1024 * ranks)))
+      break;
+  }
+  const bool apart = a.dz && (!aligned_to(a.dz, 16) || a.ld_dz % kVec != a.ld_z % kVec);
+  if (aligned_to(a.z, 16) && !apart && smem + 1024 <= kSmSmem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ranks, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr, cfg.numAttrs = ranks > 1 ? 1 : 0;
+    const int64_t room = kSmSmem / (smem + 2048), by_threads = 2 * kHeldThreads / threads;
+    int64_t an_sm = room < by_threads ? room : by_threads;
+    an_sm = an_sm < 1 ? 1 : an_sm > 32 ? 32 : an_sm;
+    auto launch = [&](auto grad, auto block) {
+      constexpr auto k = held_rows_kernel<T, decltype(grad)::value, decltype(block)::value>;
+      resident_blocks<k>(kHeldThreads, 0);  // allows it the shared memory
+      // Clusters that fit are fewer than the SMs would say, since a cluster
+      // stays within a group of SMs; one that waits for its turn would come
+      // last, with as many rows as the others had.
+      int64_t units = ranks > 1 ? resident_clusters<k>(cfg, (int)(sms * an_sm / ranks)) : sms * an_sm;
+      if (units > a.rows) units = a.rows;
+      cfg.gridDim = dim3((unsigned)(units * ranks));
+      cudaLaunchKernelEx(&cfg, k, a, workers, (int)slice);
+    };
+    auto by_block = [&](auto grad) {
+      if (threads == kHeldThreads) launch(grad, std::integral_constant<int, kHeldThreads>());
+      else if (threads == kSplitThreads) launch(grad, std::integral_constant<int, kSplitThreads>());
+      else launch(grad, std::integral_constant<int, 0>());
+    };
+    if (a.dz) by_block(std::true_type());
+    else by_block(std::false_type());
+    return;  // the caller asks for the error
+  }
+  const int64_t most = (int64_t)sms * 4;
+  rows_kernel<T><<<(unsigned)(a.rows < most ? a.rows : most), kRowThreads, 0, st>>>(a, workers);
 }
 
 struct Layout {
@@ -319,15 +817,17 @@ signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_
   WorkerRows workers = {};
   for (int m = 0; m <= n_workers; ++m) workers.begin[m] = row_begin[m];
   if (n) {
-    teacher_kernel<<<(unsigned)teacher_blocks, kTeacherWarps * 32, kTeacherWarps * top * sizeof(Entry), cs>>>(
-        n, top, top_ids, ids_int64 != 0, top_logits, top_dtype == SIGNMUON_BF16, vocab, a.inv_t,
+    int log_slots = 5;
+    while ((1 << log_slots) < 2 * top) ++log_slots;
+    resident_blocks<teacher_kernel>(kTeacherWarps * 32, 0);  // allows it the shared memory
+    teacher_kernel<<<(unsigned)teacher_blocks, kTeacherWarps * 32,
+                     kTeacherWarps * (top * sizeof(Entry) + (sizeof(int32_t) << log_slots)), cs>>>(
+        n, top, top_ids, ids_int64 != 0, top_logits, top_dtype == SIGNMUON_BF16, vocab, a.inv_t, log_slots,
         reinterpret_cast<Entry*>(ws + l.entries), reinterpret_cast<float*>(ws + l.plogp), ws + l.counts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_status(e);
-    const int64_t most = (int64_t)current_sms() * 4;
-    const unsigned grid = (unsigned)(n < most ? n : most);
-    if (dtype == SIGNMUON_F32) rows_kernel<float><<<grid, kRowThreads, 0, cs>>>(a, workers);
-    else rows_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, cs>>>(a, workers);
+    if (dtype == SIGNMUON_F32) launch_rows<float>(a, workers, cs);
+    else launch_rows<__nv_bfloat16>(a, workers, cs);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
   }
   worker_loss_kernel<<<n_workers, 256, 0, cs>>>(row_loss, a.counts, loss, workers);

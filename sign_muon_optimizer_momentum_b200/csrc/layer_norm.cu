@@ -176,7 +176,6 @@ struct Weights {
 // turn: then one barrier a sum does.
 template <int kTpr, int N>
 struct RowSum {
-  static constexpr int kWarps = kTpr / 32;
   struct Shared {
     float warp[2][kTpr > kThreads ? kTpr / 32 : kThreads / 32][N];
   };
@@ -194,9 +193,9 @@ struct RowSum {
 #pragma unroll
       for (int n = 0; n < N; ++n) v[n] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i)
+      for (int i = 0; i < kTpr / 32; ++i)
 #pragma unroll
-        for (int n = 0; n < N; ++n) v[n] += sh.warp[turn][group * kWarps + i][n];
+        for (int n = 0; n < N; ++n) v[n] += sh.warp[turn][group * (kTpr / 32) + i][n];
     }
   }
 };
