@@ -28,9 +28,11 @@ namespace {
 constexpr int kMaxTop = 1024;
 constexpr int kTeacherWarps = 4;
 constexpr int kRowThreads = 512;           // of a block that reads its row twice
-constexpr int kHeldThreads = 384;          // of a block that holds its row, at most
-constexpr int kBatch = 3;                  // chunks a thread copies as one group
-constexpr int kDepth = 5;                  // groups under way where a row is not held
+// Of a block that holds its rows (for the losses, that streams them) at most,
+// and the chunks that a thread copies as one group.
+constexpr int kHeldThreads = 384, kHeldBatch = 3;
+constexpr int kStreamThreads = 512, kStreamBatch = 4;
+constexpr int kDepth = 3;                  // groups under way where a row is not held
 constexpr int kMaxCluster = 8;
 constexpr int kSplitThreads = 256;         // ... of a block that holds a part of it, at most
 constexpr int kRowBytes = 110 * 1024;      // of a row that two blocks an SM can hold each
@@ -56,7 +58,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // ---------------------------------------------------------------- teacher
-__global__ void __launch_bounds__(kTeacherWarps * 32)
+__global__ void __launch_bounds__(kTeacherWarps * 32, 16)
 teacher_kernel(int64_t rows, int top, const void* __restrict__ ids, int wide, const void* __restrict__ logits, int bf16,
                int32_t vocab, float inv_t, int log_slots, Entry* __restrict__ entries, float* __restrict__ plogp, uint8_t* __restrict__ counts) {
   extern __shared__ Entry s_entries[];  // each warp: its entries, then its table of ids
@@ -287,13 +289,14 @@ struct RowWalk {
 };
 
 template <typename T, bool kGrad, int kThreads>
-__global__ void __launch_bounds__(kHeldThreads, 2)
+__global__ void __launch_bounds__(kGrad ? kHeldThreads : kStreamThreads, 2)
 held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, int slice) {
-  constexpr int kVec = Chunk<T>::kVec;
+  constexpr int kVec = Chunk<T>::kVec, kBatch = kGrad ? kHeldBatch : kStreamBatch;
+  constexpr int kMaxWarps = (kGrad ? kHeldThreads : kStreamThreads) / 32;
   // The block's chunks (for the losses kDepth batches), and the entries' logits.
   extern __shared__ __align__(16) uint8_t held[];
-  __shared__ Soft s_soft[2][kHeldThreads / 32], s_block[2][kMaxCluster];
-  __shared__ float s_cross[kHeldThreads / 32];
+  __shared__ Soft s_soft[2][kMaxWarps], s_block[2][kMaxCluster];
+  __shared__ float s_cross[kMaxWarps];
   __shared__ int s_n;
   const int threads = kThreads ? kThreads : blockDim.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = threads / 32;
@@ -407,45 +410,37 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
         copy_wait<kDepth - 1>();
       }
       const Chunk<T>* from = mine + (kGrad ? b : slot) * kBatch * threads;
+      Chunk<T> x[kBatch];
       if (plain(now, b)) {
-        Chunk<T> x[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) x[i] = from[i * threads];
-        float top = x[0].max();
-#pragma unroll
-        for (int i = 1; i < kBatch; ++i) top = fmaxf(top, x[i].max());
-        soft_raise(soft, top, c);
-        const Pair ref(soft_ref(soft.e), soft_ref(soft.e));
-        Pair sum(0.f, 0.f);
+      } else {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          Pair v[kVec / 2];
-          x[i].get(v);
-#pragma unroll
-          for (int q = 0; q < kVec / 2; ++q) {
-            const Pair e = fma(v[q], cc, ref);
-            sum = sum + Pair(exp2_fast(e.lo()), exp2_fast(e.hi()));
-          }
-        }
-        soft.s += sum.lo() + sum.hi();
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < kBatch && b * kBatch + i < now.n; ++i) {
           const int col = now.col + (b * kBatch + i) * stride;
-          Chunk<T> x = from[i * threads];
-          if (!whole(col)) x.r = Chunk<T>::mask(x.r, -col, a.vocab - col);
-          soft_raise(soft, x.max(), c);
-          const float ref = soft_ref(soft.e);
-          Pair v[kVec / 2], sum(0.f, 0.f);
-          x.get(v);
+          x[i].clear();
+          if (b * kBatch + i < now.n) x[i] = from[i * threads];
+          if (b * kBatch + i < now.n && !whole(col)) x[i].r = Chunk<T>::mask(x[i].r, -col, a.vocab - col);
+        }
+        __syncwarp();
+      }
+      float top = x[0].max();
 #pragma unroll
-          for (int q = 0; q < kVec / 2; ++q) {
-            const Pair e = fma(v[q], cc, Pair(ref, ref));
-            sum = sum + Pair(exp2_fast(e.lo()), exp2_fast(e.hi()));
-          }
-          soft.s += sum.lo() + sum.hi();
+      for (int i = 1; i < kBatch; ++i) top = fmaxf(top, x[i].max());
+      soft_raise(soft, top, c);
+      const Pair ref(soft_ref(soft.e), soft_ref(soft.e));
+      Pair sum(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        Pair v[kVec / 2];
+        x[i].get(v);
+#pragma unroll
+        for (int q = 0; q < kVec / 2; ++q) {
+          const Pair e = fma(v[q], cc, ref);
+          sum = sum + Pair(exp2_fast(e.lo()), exp2_fast(e.hi()));
         }
       }
+      soft.s += sum.lo() + sum.hi();
       if constexpr (!kGrad) {
         __syncwarp();
         fetch_next(slot);
@@ -717,14 +712,15 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
   // with three blocks an SM, 140 with two.)
   const int shift = a.ld_z % kVec ? kVec - 1 : 0;
   const int64_t chunks = ((int64_t)a.vocab + shift + kVec - 1) / kVec;
+  const int batch = a.dz ? kHeldBatch : kStreamBatch, most_threads = a.dz ? kHeldThreads : kStreamThreads;
   int ranks = 1, threads = 0;
   int64_t slice = 0, smem = 0;
   for (;; ranks *= 2) {
-    const int most = ranks > 1 ? kSplitThreads : kHeldThreads;
+    const int most = ranks > 1 ? kSplitThreads : most_threads;
     slice = ceil_div(chunks, ranks);
-    threads = (int)round_up((size_t)ceil_div(slice, kBatch), 32);
+    threads = (int)round_up((size_t)ceil_div(slice, batch), 32);
     if (threads > most) threads = most;
-    smem = (a.dz ? slice : (int64_t)kDepth * kBatch * threads) * 16 + (int64_t)a.top * 4;
+    smem = (a.dz ? slice : (int64_t)kDepth * batch * threads) * 16 + (int64_t)a.top * 4;
     if (ranks == kMaxCluster || !(smem > (ranks > 1 ? kSliceBytes : kRowBytes) ||
                                   (a.rows * ranks * 2 <= sms && chunks >= 1024 * ranks)))
       break;
@@ -738,12 +734,12 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)ranks, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr, cfg.numAttrs = ranks > 1 ? 1 : 0;
-    const int64_t room = kSmSmem / (smem + 2048), by_threads = 2 * kHeldThreads / threads;
+    const int64_t room = kSmSmem / (smem + 2048), by_threads = 2 * most_threads / threads;
     int64_t an_sm = room < by_threads ? room : by_threads;
     an_sm = an_sm < 1 ? 1 : an_sm > 32 ? 32 : an_sm;
     auto launch = [&](auto grad, auto block) {
       constexpr auto k = held_rows_kernel<T, decltype(grad)::value, decltype(block)::value>;
-      resident_blocks<k>(kHeldThreads, 0);  // allows it the shared memory
+      resident_blocks<k>(32, 0);  // allows it the shared memory
       // Clusters that fit are fewer than the SMs would say, since a cluster
       // stays within a group of SMs; one that waits for its turn would come
       // last, with as many rows as the others had.
@@ -753,7 +749,8 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
       cudaLaunchKernelEx(&cfg, k, a, workers, (int)slice);
     };
     auto by_block = [&](auto grad) {
-      if (threads == kHeldThreads) launch(grad, std::integral_constant<int, kHeldThreads>());
+      constexpr int kMost = decltype(grad)::value ? kHeldThreads : kStreamThreads;
+      if (threads == kMost) launch(grad, std::integral_constant<int, kMost>());
       else if (threads == kSplitThreads) launch(grad, std::integral_constant<int, kSplitThreads>());
       else launch(grad, std::integral_constant<int, 0>());
     };
