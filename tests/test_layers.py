@@ -121,27 +121,40 @@ def test_host_tensors_are_refused(lib):
             call()
 
 
-def test_shares():
-    assert list(layers._shares(8, 4, None)) == [0, 2, 4, 6, 8]
-    assert list(layers._shares(0, 3, None)) == [0, 0, 0, 0]
-    assert list(layers._shares(5, 3, [0, 0, 5, 5])) == [0, 0, 5, 5]
-    for rows, n, splits in ((7, 2, None), (4, 0, None), (4, 128, None), (4, 2, [0, 4]), (4, 2, [0, 5, 4]), (4, 2, [1, 2, 4])):
+def test_shares(lib):
+    shares = layers._load().shares
+    assert shares(8, 4, None) == [0, 2, 4, 6, 8]
+    assert shares(0, 3, None) == [0, 0, 0, 0]
+    assert shares(5, 3, [0, 0, 5, 5]) == [0, 0, 5, 5]
+    for rows, n, splits in ((7, 2, None), (4, 0, None), (4, 128, None), (4, 2, [0, 4]), (4, 2, [0, 5, 4]), (4, 2, [1, 2, 4]),
+                            (4, 2, [])):
         with pytest.raises(ValueError):
-            layers._shares(rows, n, splits)
+            shares(rows, n, splits)
 
 
-def test_rows_of_a_tensor():
+def test_rows_of_a_tensor(lib):
+    rows = layers._load().rows_of
     x = torch.zeros(6, 10)
-    assert layers._rows(x, "x") == (6, 10, 10)
-    assert layers._rows(x[:, 2:7], "x") == (6, 5, 10)
-    assert layers._rows(x[::2], "x") == (3, 10, 20)
-    assert layers._rows(x.view(2, 3, 10), "x") == (6, 10, 10)
-    assert layers._rows(x.view(2, 3, 10)[:, :, :4], "x") == (6, 4, 10)
-    assert layers._rows(x[:1, ::1], "x") == (1, 10, 10)
-    assert layers._rows(torch.zeros(0, 10), "x") == (0, 10, 10)
-    for bad in (x.t(), x[:, ::2], x[0].expand(6, 10), x.view(2, 3, 10)[:, :2], torch.zeros(4, 0), torch.tensor(1.0)):
+    assert rows(x) == (6, 10, 10)
+    assert rows(x[:, 2:7]) == (6, 5, 10)
+    assert rows(x[::2]) == (3, 10, 20)
+    assert rows(x.view(2, 3, 10)) == (6, 10, 10)
+    assert rows(x.view(2, 3, 10)[:, :, :4]) == (6, 4, 10)
+    assert rows(x.view(3, 1, 2, 10)[:, :, :, 1:]) == (6, 9, 10)
+    assert rows(x[:1, ::1]) == (1, 10, 10)
+    assert rows(torch.zeros(0, 10)) == (0, 10, 10)
+    for bad in (x.t(), x[:, ::2], x[0].expand(6, 10), x.view(2, 3, 10)[:, :2], torch.zeros(4, 0), torch.tensor(1.0),
+                x.view(2, 3, 10).transpose(0, 1)):
         with pytest.raises(ValueError):
-            layers._rows(bad, "x")
+            rows(bad)
+
+
+def test_binding_refuses_to_run_without_library(lib, tmp_path, monkeypatch):
+    monkeypatch.setattr(L, "LIB_PATH", str(tmp_path / "missing.so"))
+    monkeypatch.setattr(L, "_lib", None)
+    monkeypatch.setattr(layers, "_native", None)
+    with pytest.raises(RuntimeError, match="missing"):
+        layers.embedding_forward(torch.zeros(2, 2), torch.zeros(1, dtype=torch.int64))
 
 
 # ---------------------------------------------------------------- GPU parity
