@@ -10,15 +10,17 @@
 //   1. sort   Each worker's (id, token) pairs are sorted by id in tiles of
 //             kTile, a block a tile, in shared memory (stable counting passes
 //             of up to 9 bits).  The other blocks of the launch meanwhile fill
-//             the tables with zeros: the sort is bound by latency and takes
-//             few SMs, the fill is bound by HBM.
+//             the first rows of the tables with zeros: the sort is bound by
+//             latency and takes few SMs, the fill is bound by HBM.
 //   2. merge  Only for workers of more than one tile: each pair's place is its
 //             place in its own run plus the smaller pairs of the other runs,
 //             found by binary search, kFan runs at a time.
-//   3. reduce A warp takes kChunk consecutive sorted pairs and a slab of
-//             columns, adds the rows of each run of equal ids in registers and
+//   3. reduce A warp takes a chunk of consecutive sorted pairs (32, or 8 where
+//             that leaves SMs without work) and a slab of columns, adds the rows of each run of equal ids in registers and
 //             writes the runs that lie within the chunk.  What a run that
 //             crosses a chunk's ends has there is left as a partial row.
+//             Other blocks of the launch fill the tables' other rows with
+//             zeros, those that no id names.
 //   4. join   The chunk where such a run begins adds its partial rows and
 //             writes the row; long runs (frequent tokens) by a whole block.
 #include "layers.cuh"
@@ -35,9 +37,13 @@ constexpr int kTile = kSortThreads * kSortItems;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kFan = 32;             // runs merged at a time
+constexpr int64_t kFillBeside = 40 << 20;  // bytes that are filled in the time of a sort
+// Runs merged at a time: as many as a thread searches side by side.  (100003
+// tokens: 5 us for tiles of 4096 and 11 for each of two merges; tiles of 16384
+// took 33, and one merge of 32 runs 31.)
+constexpr int kFan = 8;
 constexpr int kMergeThreads = 256;
-constexpr int kChunk = 32;           // sorted pairs a warp of the reduction takes
+constexpr int kLongChunk = 32, kShortChunk = 8;  // sorted pairs a warp of the reduction takes
 constexpr int kLaneCols = 8;         // columns of a lane's slab
 constexpr int kSlab = 32 * kLaneCols;
 constexpr int kReduceThreads = 256;
@@ -71,7 +77,10 @@ lookup_kernel(const TW* __restrict__ table, int64_t ld_table, int32_t vocab, int
       if (in) unpack(raw[i], v);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[j] = in ? v[j] * scale : 0.f;
-      store_stream<TY, VEC>(y + token * ld_y + col, v);
+      // Narrow stores share 32-byte sectors with others': those are left to L2
+      // to put together.
+      if (VEC * sizeof(TY) >= 8) store_stream<TY, VEC>(y + token * ld_y + col, v);
+      else store_vec<TY, VEC>(y + token * ld_y + col, v);
     }
   }
 }
@@ -79,22 +88,22 @@ lookup_kernel(const TW* __restrict__ table, int64_t ld_table, int32_t vocab, int
 // ------------------------------------------------------------ sort and fill
 struct Fill {
   WorkerPtrs grad;
-  int64_t bytes;  // of one table; 0: nothing to fill
+  int64_t row_bytes;  // of a table's row
+  int32_t rows;       // of a table; 0: nothing to fill
+  int32_t head;       // rows that the sort's launch fills
 };
 
-__device__ void fill_zero(const Fill& f, int n_workers, int block, int blocks) {
+// Zeros from p on, by `threads` threads of which this is the t-th: the ends
+// that are not whole 16 bytes two bytes at a time.
+__device__ __forceinline__ void zero_bytes(uint8_t* p, int64_t bytes, int64_t t, int64_t threads) {
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int m = 0; m < n_workers; ++m) {
-    uint8_t* p = static_cast<uint8_t*>(f.grad.p[m]);
-    // The ends that are not whole 16 bytes, two bytes at a time.
-    const int64_t head = min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15), f.bytes);
-    const int64_t n16 = (f.bytes - head) / 16, tail = head + n16 * 16;
-    if (block == 0) {
-      for (int64_t i = threadIdx.x * 2; i < head; i += kSortThreads * 2) *reinterpret_cast<uint16_t*>(p + i) = 0;
-      for (int64_t i = tail + threadIdx.x * 2; i < f.bytes; i += kSortThreads * 2) *reinterpret_cast<uint16_t*>(p + i) = 0;
-    }
-    uint4* q = reinterpret_cast<uint4*>(p + head);
-    for (int64_t i = (int64_t)block * kSortThreads + threadIdx.x; i < n16; i += (int64_t)blocks * kSortThreads) __stcs(q + i, zero);
+  const int64_t head = min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15), bytes);
+  const int64_t n16 = (bytes - head) / 16, tail = head + n16 * 16;
+  uint4* q = reinterpret_cast<uint4*>(p + head);
+  for (int64_t i = t; i < n16; i += threads) __stcs(q + i, zero);
+  if (t < 8) {
+    if (2 * t < head) *reinterpret_cast<uint16_t*>(p + 2 * t) = 0;
+    if (tail + 2 * t < bytes) *reinterpret_cast<uint16_t*>(p + tail + 2 * t) = 0;
   }
 }
 
@@ -104,14 +113,16 @@ __global__ void __launch_bounds__(kSortThreads)
 sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks tiles, int n_workers,
                   const void* __restrict__ ids, int wide, uint32_t vocab, int passes, int bits, uint32_t* __restrict__ out_key,
                   uint32_t* __restrict__ out_tok, const __grid_constant__ Fill fill) {
-  __shared__ uint32_t s_key[kTile];
-  __shared__ uint16_t s_tok[kTile];
-  extern __shared__ uint16_t s_count[];  // [kSortWarps][kDigits]
+  extern __shared__ uint32_t s_key[];                                    // [kTile]
+  uint16_t* s_tok = reinterpret_cast<uint16_t*>(s_key + kTile);          // [kTile]
+  uint16_t* s_count = s_tok + kTile;                                     // [kSortWarps][kDigits]
   __shared__ uint32_t s_digit[kDigits];  // first place of each digit
   __shared__ uint32_t s_warp[kSortWarps];
   const int n_tiles = tiles.begin[n_workers];
   if ((int)blockIdx.x >= n_tiles) {
-    fill_zero(fill, n_workers, blockIdx.x - n_tiles, gridDim.x - n_tiles);
+    const int64_t t = (int64_t)(blockIdx.x - n_tiles) * kSortThreads + threadIdx.x;
+    for (int m = 0; m < n_workers; ++m)
+      zero_bytes(static_cast<uint8_t*>(fill.grad.p[m]), fill.head * fill.row_bytes, t, (int64_t)(gridDim.x - n_tiles) * kSortThreads);
     return;
   }
   const int m = worker_of_block(tiles, n_workers, blockIdx.x);
@@ -119,29 +130,37 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
   const int n = (int)min((int64_t)kTile, rows.begin[m + 1] - base);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int first = warp * 32 * kSortItems + lane;  // this thread's items: first + 32 j
-  uint32_t key[kSortItems], tok[kSortItems];
+  // at[j]: the pair's token in the tile, and above it its rank among the warp's
+  // pairs with the same digit (both at most 2^14).
+  uint32_t key[kSortItems], at[kSortItems];
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
     const int i = first + 32 * j;
     int64_t id = -1;
     if (i < n) id = load_id(ids, base + i, wide);
     key[j] = id >= 0 && id < (int64_t)vocab ? (uint32_t)id : vocab;
-    tok[j] = i;
+    at[j] = i;
   }
-  const uint32_t mask = (1u << bits) - 1;
+  const uint32_t mask = (1u << bits) - 1, lower = (1u << lane) - 1;
   uint16_t* count = s_count + warp * kDigits;
   for (int pass = 0; pass < passes; ++pass) {
     const int shift = pass * bits;
-    for (int i = lane; i < kDigits; i += 32) count[i] = 0;
+    for (int i = lane; i < kDigits / 2; i += 32) reinterpret_cast<uint32_t*>(count)[i] = 0;
     __syncwarp();
-    uint32_t rank[kSortItems];
 #pragma unroll
     for (int j = 0; j < kSortItems; ++j) {
       const uint32_t d = key[j] >> shift & mask;
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      const uint32_t before = peers & ((1u << lane) - 1);
-      const uint32_t seen = count[d];
-      rank[j] = seen + __popc(before);
+      // The lanes with the same digit, bit by bit (__match_any_sync takes as
+      // long for each of the digits that there are).
+      uint32_t peers = 0xffffffffu;
+#pragma unroll
+      for (int i = 0; i < kDigitBits; ++i) {
+        const bool set = d >> i & 1;
+        const uint32_t with = __ballot_sync(0xffffffffu, set);
+        peers &= set ? with : ~with;
+      }
+      const uint32_t seen = count[d], before = __popc(peers & lower);
+      at[j] |= (seen + before) << 16;
       __syncwarp();
       if (before == 0) count[d] = (uint16_t)(seen + __popc(peers));
       __syncwarp();
@@ -150,11 +169,16 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
     // Counts to places: by digit, within a digit by warp.
     uint32_t total = 0;
     if (threadIdx.x < kDigits) {
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = s_count[w * kDigits + threadIdx.x];
-        s_count[w * kDigits + threadIdx.x] = (uint16_t)total;
-        total += c;
+#pragma unroll
+      for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
+        uint32_t c[16];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) c[w] = s_count[(w0 + w) * kDigits + threadIdx.x];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+          s_count[(w0 + w) * kDigits + threadIdx.x] = (uint16_t)total;
+          total += c[w];
+        }
       }
     }
     uint32_t scan = total;
@@ -166,27 +190,27 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
     if (lane == 31) s_warp[warp] = scan;
     __syncthreads();
     if (threadIdx.x < kDigits) {
-      uint32_t lower = 0;
-      for (int w = 0; w < warp; ++w) lower += s_warp[w];
-      s_digit[threadIdx.x] = lower + scan - total;
+      uint32_t below = lane < warp ? s_warp[lane] : 0;
+      below = __reduce_add_sync(0xffffffffu, below);
+      s_digit[threadIdx.x] = below + scan - total;
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kSortItems; ++j) {
       const uint32_t d = key[j] >> shift & mask;
-      const uint32_t at = s_digit[d] + count[d] + rank[j];
-      s_key[at] = key[j];
-      s_tok[at] = (uint16_t)tok[j];
+      const uint32_t to = s_digit[d] + count[d] + (at[j] >> 16);
+      s_key[to] = key[j];
+      s_tok[to] = (uint16_t)at[j];
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) key[j] = s_key[first + 32 * j], tok[j] = s_tok[first + 32 * j];
+    for (int j = 0; j < kSortItems; ++j) key[j] = s_key[first + 32 * j], at[j] = s_tok[first + 32 * j];
     __syncthreads();
   }
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
     const int i = first + 32 * j;
-    if (i < n) out_key[base + i] = key[j], out_tok[base + i] = (uint32_t)(base + tok[j]);
+    if (i < n) out_key[base + i] = key[j], out_tok[base + i] = (uint32_t)base + at[j];
   }
 }
 
@@ -206,30 +230,27 @@ merge_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ Wo
   const int mine = p / run, group = mine / kFan * kFan, own = mine - group;
   const int runs = min(kFan, (n + run - 1) / run - group);
   // Pairs of the other runs that go before: keys below k, and equal ones of
-  // an earlier run.  kBatch searches go side by side, without branches: one
-  // alone would wait for each of its loads.
-  constexpr int kBatch = 8;
-  int before = 0;
-  for (int i0 = 0; i0 < runs; i0 += kBatch) {
-    int at[kBatch];
+  // an earlier run.  The searches go side by side, without branches: one alone
+  // would wait for each of its loads.
+  int at[kFan];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) at[i] = 0;
-    for (int step = run; step; step /= 2) {
-      uint32_t seen[kBatch];
+  for (int i = 0; i < kFan; ++i) at[i] = 0;
+  for (int step = run; step; step /= 2) {
+    uint32_t seen[kFan];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int begin = (group + min(i0 + i, runs - 1)) * run;
-        seen[i] = key[begin + min(at[i] + step, min(run, n - begin)) - 1];
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int begin = (group + min(i0 + i, runs - 1)) * run, probe = at[i] + step;
-        at[i] = probe <= min(run, n - begin) && seen[i] < k + (i0 + i < own ? 1u : 0u) ? probe : at[i];
-      }
+    for (int i = 0; i < kFan; ++i) {
+      const int begin = (group + min(i, runs - 1)) * run;
+      seen[i] = key[begin + min(at[i] + step, min(run, n - begin)) - 1];
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) before += i0 + i < runs && i0 + i != own ? at[i] : 0;
+    for (int i = 0; i < kFan; ++i) {
+      const int begin = (group + min(i, runs - 1)) * run, probe = at[i] + step;
+      at[i] = probe <= min(run, n - begin) && seen[i] < k + (i < own ? 1u : 0u) ? probe : at[i];
+    }
   }
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < kFan; ++i) before += i < runs && i != own ? at[i] : 0;
   const int64_t place = rows.begin[m] + (int64_t)group * run + (p - mine * run) + before;
   out_key[place] = k;
   out_tok[place] = tok[rows.begin[m] + p];
@@ -241,10 +262,17 @@ struct ReduceArgs {
   const uint32_t* tok;
   const void* dy;
   int64_t ld_dy;
-  float* part;  // [chunks][2][cols]: what the run from the chunk before, and the one into the next, have here
+  // [chunks][2][slabs][2][32 lanes] of four floats: what the run from the chunk
+  // before, and the one into the next, have here, as the lanes hold it.
+  float4* part;
   uint32_t vocab;
-  int32_t cols, n_workers, accumulate;
+  int32_t chunk;  // pairs of a chunk
+  int32_t cols, slabs, n_workers, accumulate;
+  int32_t n_blocks;  // of the reduction; further blocks of its launch fill
   float scale;
+  __device__ __forceinline__ float4* partial(int chunk_, int which, int slab) const {
+    return part + (((int64_t)chunk_ * 2 + which) * slabs + slab) * 64 + (threadIdx.x & 31);
+  }
 };
 
 // One chunk of a worker's sorted pairs.
@@ -259,22 +287,63 @@ __device__ __forceinline__ Chunk chunk_at(const ReduceArgs& a, const WorkerRows&
                                           int chunk) {
   Chunk c;
   const int lane = threadIdx.x & 31;
-  c.begin = rows.begin[m] + (int64_t)(chunk - chunks.begin[m]) * kChunk;
+  const int last = a.chunk - 1;
+  c.begin = rows.begin[m] + (int64_t)(chunk - chunks.begin[m]) * a.chunk;
   const int64_t end = rows.begin[m + 1];
-  const bool in = c.begin + lane < end;
+  const bool in = lane <= last && c.begin + lane < end;
   c.key = in ? a.key[c.begin + lane] : a.vocab;
   // The neighbours' keys; vocab where there is none, which equals no key here.
   uint32_t edge = a.vocab;
   if (lane == 0 && c.begin > rows.begin[m]) edge = a.key[c.begin - 1];
-  if (lane == 31 && c.begin + kChunk < end) edge = a.key[c.begin + kChunk];
+  if (lane == last && c.begin + a.chunk < end) edge = a.key[c.begin + a.chunk];
   c.n = __popc(__ballot_sync(0xffffffffu, c.key < a.vocab));
   uint32_t after = __shfl_down_sync(0xffffffffu, c.key, 1);
-  if (lane == 31) after = edge;
+  if (lane == last) after = edge;
   c.ends = __ballot_sync(0xffffffffu, c.key < a.vocab && c.key != after);
   const uint32_t joins = __ballot_sync(0xffffffffu, c.key < a.vocab && c.key == edge);
   c.from_before = joins & 1u;
-  c.into_next = joins >> 31;
+  c.into_next = joins >> last & 1u;
   return c;
+}
+
+// First of the sorted keys [lo, hi) that is above `key` (kAbove) or not below
+// it, by a warp, 32 probes at a time.
+template <bool kAbove>
+__device__ __forceinline__ int64_t find_key(const uint32_t* keys, int64_t lo, int64_t hi, uint32_t key) {
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 31) / 32, probe = lo + (threadIdx.x & 31) * step + step - 1;
+    const bool below = probe < hi && (kAbove ? keys[probe] <= key : keys[probe] < key);
+    lo = min(hi, lo + __popc(__ballot_sync(0xffffffffu, below)) * step);
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+// Fills rows 32 u .. 32 u + 31 of those that the sort's launch left, of all
+// tables in turn, where no id names them.
+__device__ __forceinline__ void fill_rest(const ReduceArgs& a, const WorkerRows& rows, const Fill& fill, int64_t u) {
+  const int per_table = (fill.rows - fill.head + 31) / 32, lane = threadIdx.x & 31;
+  const int m = (int)(u / per_table);
+  if (m >= a.n_workers) return;
+  const uint32_t first = fill.head + (uint32_t)(u % per_table) * 32, last = min(first + 32, (uint32_t)fill.rows);
+  uint32_t named = last - first < 32 ? ~0u << (last - first) : 0u;  // rows that are not to be filled
+  const int64_t end = rows.begin[m + 1];
+  for (int64_t at = find_key<false>(a.key, rows.begin[m], end, first); at < end; at += 32) {
+    const uint32_t key = at + lane < end ? a.key[at + lane] : a.vocab;
+    named |= __reduce_or_sync(0xffffffffu, key < last ? 1u << (key - first) : 0u);
+    const uint32_t far = __shfl_sync(0xffffffffu, key, 31);
+    if (far >= last) break;
+    // Past the rest of a long run at once.
+    if (far == __shfl_sync(0xffffffffu, key, 0)) at = find_key<true>(a.key, at + 32, end, far) - 32;
+  }
+  uint8_t* table = static_cast<uint8_t*>(fill.grad.p[m]);
+  while (~named) {
+    const int begin = __ffs(~named) - 1;
+    const uint32_t after = named >> begin;
+    const int n = after ? __ffs(after) - 1 : 32 - begin;
+    zero_bytes(table + (int64_t)(first + begin) * fill.row_bytes, n * fill.row_bytes, lane, 32);
+    named |= (n == 32 ? ~0u : (1u << n) - 1) << begin;
+  }
 }
 
 template <typename TG, int VEC>
@@ -295,25 +364,27 @@ __device__ __forceinline__ void write_grad(TG* row, int col0, int cols, int accu
 template <typename TD, typename TG, int VEC>
 __global__ void __launch_bounds__(kReduceThreads)
 reduce_kernel(const ReduceArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks chunks,
-              const __grid_constant__ WorkerPtrs grad) {
+              const __grid_constant__ Fill fill) {
   constexpr int kVecs = kLaneCols / VEC, kBatch = 4;
-  const int lane = threadIdx.x & 31, chunk = blockIdx.x * (kReduceThreads / 32) + threadIdx.x / 32;
+  if ((int)blockIdx.x >= a.n_blocks) {
+    fill_rest(a, rows, fill, (int64_t)(blockIdx.x - a.n_blocks) * (kReduceThreads / 32) + threadIdx.x / 32);
+    return;
+  }
+  const int lane = threadIdx.x & 31, slab = blockIdx.x % a.slabs;
+  const int chunk = blockIdx.x / a.slabs * (kReduceThreads / 32) + threadIdx.x / 32;
   if (chunk >= chunks.begin[a.n_workers]) return;
   const int m = worker_of_block(chunks, a.n_workers, chunk);
   const Chunk c = chunk_at(a, rows, chunks, m, chunk);
   const uint32_t tok = lane < c.n ? a.tok[c.begin + lane] : 0;
-  const int col0 = blockIdx.y * kSlab + lane * VEC, cols = a.cols;
+  const int col0 = slab * kSlab + lane * VEC, cols = a.cols;
   const TD* dy = static_cast<const TD*>(a.dy);
-  TG* table = static_cast<TG*>(grad.p[m]);
-  float* part = a.part + (int64_t)chunk * 2 * cols;
+  TG* table = static_cast<TG*>(fill.grad.p[m]);
   float acc[kLaneCols] = {};
   bool first = true;
   auto write_part = [&](int which) {
-#pragma unroll
-    for (int i = 0; i < kLaneCols; ++i) {
-      const int col = col0 + i / VEC * 32 * VEC + i % VEC;
-      if (col < cols) part[which * cols + col] = acc[i];
-    }
+    float4* p = a.partial(chunk, which, slab);
+    p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    p[32] = make_float4(acc[4], acc[5], acc[6], acc[7]);
   };
   for (int j0 = 0; j0 < c.n; j0 += kBatch) {
     typename RawVec<TD, VEC>::type raw[kBatch][kVecs];
@@ -362,36 +433,43 @@ join_kernel(const ReduceArgs a, const __grid_constant__ WorkerRows rows, const _
   __shared__ int s_worker[kJoinChunks];
   __shared__ float s_acc[kJoinChunks][kSlab];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, cols = a.cols;
-  const int chunk0 = blockIdx.x * kJoinChunks, chunk = chunk0 + warp;
-  const int col0 = blockIdx.y * kSlab + lane * VEC;
+  const int chunk0 = blockIdx.x * kJoinChunks, chunk = chunk0 + warp, slab = blockIdx.y;
+  const int col0 = slab * kSlab + lane * VEC;
   int follow = 0, m = 0;
   uint32_t key = 0;
   if (chunk < chunks.begin[a.n_workers]) {
     m = worker_of_block(chunks, a.n_workers, chunk);
     const Chunk c = chunk_at(a, rows, chunks, m, chunk);
-    key = __shfl_sync(0xffffffffu, c.key, 31);
+    key = __shfl_sync(0xffffffffu, c.key, a.chunk - 1);
     // A run that begins here (this chunk is not all one run from before) and
     // goes on: how many chunks it goes on in.
     if (c.into_next && (c.ends || !c.from_before)) {
-      int64_t lo = c.begin + kChunk + 1, hi = rows.begin[m + 1];
-      while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.key[mid] <= key) lo = mid + 1;
-        else hi = mid;
-      }
-      follow = (int)((lo - (c.begin + kChunk) + kChunk - 1) / kChunk);
+      // By the first keys of the 32 chunks after the next, or else by search.
+      const int64_t begin = c.begin + a.chunk, end = rows.begin[m + 1], probe = begin + (int64_t)(1 + lane) * a.chunk;
+      const uint32_t same = __ballot_sync(0xffffffffu, probe < end && a.key[probe] == key);
+      follow = same != 0xffffffffu ? __ffs(~same)
+                                   : (int)((find_key<true>(a.key, begin + 1, end, key) - begin + a.chunk - 1) / a.chunk);
     }
   }
   // Adds the partial rows of chunk + i for i = from, from + step, ... <= n.
   auto add = [&](int at, int from, int step, int n, float (&acc)[kLaneCols]) {
-#pragma unroll 4
-    for (int i = from; i <= n; i += step) {
-      const float* p = a.part + ((int64_t)(at + i) * 2 + (i == 0 ? 1 : 0)) * cols;
+    constexpr int kBatch = 8;
+    for (int i0 = from; i0 <= n; i0 += kBatch * step) {
+      float4 p[kBatch][2];
 #pragma unroll
-      for (int q = 0; q < kLaneCols; ++q) {
-        const int col = col0 + q / VEC * 32 * VEC + q % VEC;
-        if (col < cols) acc[q] += p[col];
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * step;
+        if (i <= n) {
+          const float4* q = a.partial(at + i, i == 0 ? 1 : 0, slab);
+          p[j][0] = q[0], p[j][1] = q[32];
+        }
       }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i0 + j * step <= n) {
+          acc[0] += p[j][0].x, acc[1] += p[j][0].y, acc[2] += p[j][0].z, acc[3] += p[j][0].w;
+          acc[4] += p[j][1].x, acc[5] += p[j][1].y, acc[6] += p[j][1].z, acc[7] += p[j][1].w;
+        }
     }
   };
   const bool is_long = follow >= kLongRun;
@@ -426,10 +504,16 @@ join_kernel(const ReduceArgs a, const __grid_constant__ WorkerRows rows, const _
 struct BackwardLayout {
   size_t key[2], tok[2], part, total;
 };
-int64_t chunks_of(const int64_t* row_begin, int n_workers) {
+int64_t chunks_of(const int64_t* row_begin, int n_workers, int chunk) {
   int64_t n = 0;
-  for (int m = 0; m < n_workers; ++m) n += ceil_div(row_begin[m + 1] - row_begin[m], kChunk);
+  for (int m = 0; m < n_workers; ++m) n += ceil_div(row_begin[m + 1] - row_begin[m], chunk);
   return n;
+}
+// Short chunks where long ones would leave SMs without a warp in each
+// scheduler: a warp's loads of rows wait for one another.
+int chunk_pairs(int32_t cols, int n_workers, const int64_t* row_begin) {
+  return chunks_of(row_begin, n_workers, kLongChunk) * ceil_div(cols, kSlab) < 4 * (int64_t)current_sms() ? kShortChunk
+                                                                                                      : kLongChunk;
 }
 BackwardLayout backward_layout(int32_t cols, int n_workers, const int64_t* row_begin) {
   const size_t n = round_up((size_t)row_begin[n_workers] * 4, 256);
@@ -439,7 +523,7 @@ BackwardLayout backward_layout(int32_t cols, int n_workers, const int64_t* row_b
   l.tok[0] = l.key[1] + n;
   l.tok[1] = l.tok[0] + n;
   l.part = l.tok[1] + n;
-  l.total = l.part + round_up((size_t)chunks_of(row_begin, n_workers) * 2 * cols * 4, 256);
+  l.total = l.part + round_up((size_t)chunks_of(row_begin, n_workers, chunk_pairs(cols, n_workers, row_begin)) * 2 * ceil_div(cols, kSlab) * kSlab * 4, 256);
   return l;
 }
 
@@ -552,16 +636,20 @@ signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_wo
   while (key_bits < 31 && (table_shape.rows >> key_bits)) ++key_bits;
   const int passes = (key_bits + kDigitBits - 1) / kDigitBits, bits = (key_bits + passes - 1) / passes;
   const WorkerBlocks tiles = blocks_of(row_begin, n_workers, kTile);
-  fill.bytes = accumulate ? 0 : (int64_t)table_shape.rows * cols * dtype_bytes(grad_dtype);
-  int64_t fill_blocks = accumulate ? 0 : ceil_div(fill.bytes * n_workers, 65536);
+  // The sort's launch fills what it has the time for (kFillBeside bytes), the
+  // reduction's the rest.
+  fill.rows = accumulate ? 0 : table_shape.rows;
+  fill.row_bytes = (int64_t)cols * dtype_bytes(grad_dtype);
+  const int64_t head = kFillBeside / (fill.row_bytes * n_workers) + 1;
+  fill.head = (int32_t)(n == 0 || head > fill.rows ? fill.rows : head);
+  int64_t fill_blocks = ceil_div(fill.head * fill.row_bytes * n_workers, 65536);
   if (fill_blocks > 2 * current_sms()) fill_blocks = 2 * current_sms();
   const int64_t grid = tiles.begin[n_workers] + fill_blocks;
   if (!grid) return SIGNMUON_OK;
-  constexpr int kCountBytes = kSortWarps * kDigits * 2;
-  resident_blocks<sort_tiles_kernel>(kSortThreads, kCountBytes);  // allows it the shared memory
-  sort_tiles_kernel<<<(unsigned)grid, kSortThreads, kCountBytes, cs>>>(rows, tiles, n_workers, ids, ids_int64 != 0,
-                                                                      (uint32_t)table_shape.rows, passes, bits, key[0], tok[0],
-                                                                      fill);
+  constexpr size_t kSmem = (size_t)kTile * 6 + kSortWarps * kDigits * 2;
+  resident_blocks<sort_tiles_kernel>(kSortThreads, kSmem);  // allows it the shared memory
+  sort_tiles_kernel<<<(unsigned)grid, kSortThreads, kSmem, cs>>>(rows, tiles, n_workers, ids, ids_int64 != 0,
+                                                                (uint32_t)table_shape.rows, passes, bits, key[0], tok[0], fill);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
   if (!n) return SIGNMUON_OK;
@@ -574,18 +662,24 @@ signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_wo
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
   }
 
-  const WorkerBlocks chunks = blocks_of(row_begin, n_workers, kChunk);
+  const int chunk = chunk_pairs(cols, n_workers, row_begin);
+  const WorkerBlocks chunks = blocks_of(row_begin, n_workers, chunk);
   const int n_chunks = chunks.begin[n_workers];
   ReduceArgs a = {};
-  a.key = key[at], a.tok = tok[at], a.dy = dy, a.ld_dy = ld_dy, a.part = reinterpret_cast<float*>(ws + l.part);
-  a.vocab = (uint32_t)table_shape.rows, a.cols = cols, a.n_workers = n_workers, a.accumulate = accumulate != 0, a.scale = scale;
-  const unsigned slabs = (unsigned)ceil_div(cols, kSlab);
+  a.key = key[at], a.tok = tok[at], a.dy = dy, a.ld_dy = ld_dy, a.part = reinterpret_cast<float4*>(ws + l.part);
+  a.vocab = (uint32_t)table_shape.rows, a.chunk = chunk, a.cols = cols, a.n_workers = n_workers, a.accumulate = accumulate != 0, a.scale = scale;
+  a.slabs = (int32_t)ceil_div(cols, kSlab);
+  const int64_t reduce_blocks = ceil_div(n_chunks, kReduceThreads / 32) * a.slabs;
+  const int64_t rest = ceil_div((int64_t)fill.rows - fill.head, 32) * n_workers;
+  if (reduce_blocks + ceil_div(rest, kReduceThreads / 32) > INT32_MAX) return SIGNMUON_ERR_UNSUPPORTED;
+  a.n_blocks = (int32_t)reduce_blocks;
+  const unsigned blocks = (unsigned)(reduce_blocks + ceil_div(rest, kReduceThreads / 32));
   by_types(dy_dtype, grad_dtype, vec, [&](auto td, auto tg, auto v) {
-    reduce_kernel<decltype(td), decltype(tg), decltype(v)::value>
-        <<<dim3((unsigned)ceil_div(n_chunks, kReduceThreads / 32), slabs), kReduceThreads, 0, cs>>>(a, rows, chunks, fill.grad);
+    reduce_kernel<decltype(td), decltype(tg), decltype(v)::value><<<blocks, kReduceThreads, 0, cs>>>(a, rows, chunks, fill);
     if ((e = cudaGetLastError()) != cudaSuccess) return;
     join_kernel<decltype(tg), decltype(v)::value>
-        <<<dim3((unsigned)ceil_div(n_chunks, kJoinChunks), slabs), kJoinChunks * 32, 0, cs>>>(a, rows, chunks, fill.grad);
+        <<<dim3((unsigned)ceil_div(n_chunks, kJoinChunks), (unsigned)a.slabs), kJoinChunks * 32, 0, cs>>>(a, rows, chunks,
+                                                                                                       fill.grad);
     e = cudaGetLastError();
   });
   return cuda_status(e);

@@ -245,7 +245,8 @@ EMBED_BACKWARD = [
     ([4096], 513, 40, "uniform", 0),
     ([4097, 12289], 60000, 24, "zipf", 0),
     ([20000], 3, 17, "uniform", 1),
-    ([140000], 263000, 8, "zipf", 0),           # more than 32 sorted tiles: two merges
+    ([40000], 70000, 8, "zipf", 0),             # more than eight sorted tiles: two merges
+    ([270000, 7], 263000, 4, "zipf", 0),        # more than 64: three
     ([9000], 1, 300, "same", 0),
     ([700] * 9, 128, 770, "zipf", 0),
 ]
