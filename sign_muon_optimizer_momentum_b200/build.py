@@ -57,7 +57,7 @@ def _link_binding(obj: str) -> None:
     import torch
     tmp = BINDING + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-lsignmuon", "-Wl,-rpath,$ORIGIN",
-           f"-L{os.path.join(os.path.dirname(torch.__file__), 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           f"-L{os.path.join(os.path.dirname(torch.__file__), 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch",
            "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

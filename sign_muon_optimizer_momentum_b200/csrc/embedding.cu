@@ -91,6 +91,7 @@ struct Fill {
   int64_t row_bytes;  // of a table's row
   int32_t rows;       // of a table; 0: nothing to fill
   int32_t head;       // rows that the sort's launch fills
+  int32_t unit;       // rows that a warp of the reduction's launch fills (at most 32)
 };
 
 // Zeros from p on, by `threads` threads of which this is the t-th: the ends
@@ -142,41 +143,45 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
     at[j] = i;
   }
   const uint32_t mask = (1u << bits) - 1, lower = (1u << lane) - 1;
+  // Warps that have pairs (the last one's missing pairs have the last key).
+  const int used = (n + 32 * kSortItems - 1) / (32 * kSortItems);
   uint16_t* count = s_count + warp * kDigits;
   for (int pass = 0; pass < passes; ++pass) {
     const int shift = pass * bits;
-    for (int i = lane; i < kDigits / 2; i += 32) reinterpret_cast<uint32_t*>(count)[i] = 0;
-    __syncwarp();
+    if (warp < used) {
+      for (int i = lane; i < kDigits / 2; i += 32) reinterpret_cast<uint32_t*>(count)[i] = 0;
+      __syncwarp();
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
-      const uint32_t d = key[j] >> shift & mask;
-      // The lanes with the same digit, bit by bit (__match_any_sync takes as
-      // long for each of the digits that there are).
-      uint32_t peers = 0xffffffffu;
+      for (int j = 0; j < kSortItems; ++j) {
+        const uint32_t d = key[j] >> shift & mask;
+        // The lanes with the same digit, bit by bit (4096 pairs: 10 us in all;
+        // with __match_any_sync, which takes as long for each of the digits
+        // that there are, 13).
+        uint32_t peers = 0xffffffffu;
 #pragma unroll
-      for (int i = 0; i < kDigitBits; ++i) {
-        const bool set = d >> i & 1;
-        const uint32_t with = __ballot_sync(0xffffffffu, set);
-        peers &= set ? with : ~with;
+        for (int i = 0; i < kDigitBits; ++i) {
+          const bool set = d >> i & 1;
+          const uint32_t with = __ballot_sync(0xffffffffu, set);
+          peers &= set ? with : ~with;
+        }
+        const uint32_t seen = count[d], before = __popc(peers & lower);
+        at[j] |= (seen + before) << 16;
+        __syncwarp();
+        if (before == 0) count[d] = (uint16_t)(seen + __popc(peers));
+        __syncwarp();
       }
-      const uint32_t seen = count[d], before = __popc(peers & lower);
-      at[j] |= (seen + before) << 16;
-      __syncwarp();
-      if (before == 0) count[d] = (uint16_t)(seen + __popc(peers));
-      __syncwarp();
     }
     __syncthreads();
     // Counts to places: by digit, within a digit by warp.
     uint32_t total = 0;
     if (threadIdx.x < kDigits) {
+      for (int w0 = 0; w0 < used; w0 += 8) {
+        uint32_t c[8];
 #pragma unroll
-      for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
-        uint32_t c[16];
+        for (int w = 0; w < 8; ++w) c[w] = w0 + w < used ? s_count[(w0 + w) * kDigits + threadIdx.x] : 0;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) c[w] = s_count[(w0 + w) * kDigits + threadIdx.x];
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-          s_count[(w0 + w) * kDigits + threadIdx.x] = (uint16_t)total;
+        for (int w = 0; w < 8; ++w) {
+          if (w0 + w < used) s_count[(w0 + w) * kDigits + threadIdx.x] = (uint16_t)total;
           total += c[w];
         }
       }
@@ -195,16 +200,18 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
       s_digit[threadIdx.x] = below + scan - total;
     }
     __syncthreads();
+    if (warp < used)
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
-      const uint32_t d = key[j] >> shift & mask;
-      const uint32_t to = s_digit[d] + count[d] + (at[j] >> 16);
-      s_key[to] = key[j];
-      s_tok[to] = (uint16_t)at[j];
-    }
+      for (int j = 0; j < kSortItems; ++j) {
+        const uint32_t d = key[j] >> shift & mask;
+        const uint32_t to = s_digit[d] + count[d] + (at[j] >> 16);
+        s_key[to] = key[j];
+        s_tok[to] = (uint16_t)at[j];
+      }
     __syncthreads();
+    if (warp < used)
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) key[j] = s_key[first + 32 * j], at[j] = s_tok[first + 32 * j];
+      for (int j = 0; j < kSortItems; ++j) key[j] = s_key[first + 32 * j], at[j] = s_tok[first + 32 * j];
     __syncthreads();
   }
 #pragma unroll
@@ -319,13 +326,14 @@ __device__ __forceinline__ int64_t find_key(const uint32_t* keys, int64_t lo, in
   return lo;
 }
 
-// Fills rows 32 u .. 32 u + 31 of those that the sort's launch left, of all
-// tables in turn, where no id names them.
+// Fills the u-th `unit` rows of those that the sort's launch left, of all tables
+// in turn, where no id names them.
 __device__ __forceinline__ void fill_rest(const ReduceArgs& a, const WorkerRows& rows, const Fill& fill, int64_t u) {
-  const int per_table = (fill.rows - fill.head + 31) / 32, lane = threadIdx.x & 31;
+  const int per_table = (fill.rows - fill.head + fill.unit - 1) / fill.unit, lane = threadIdx.x & 31;
   const int m = (int)(u / per_table);
   if (m >= a.n_workers) return;
-  const uint32_t first = fill.head + (uint32_t)(u % per_table) * 32, last = min(first + 32, (uint32_t)fill.rows);
+  const uint32_t first = fill.head + (uint32_t)(u % per_table) * fill.unit;
+  const uint32_t last = min(first + fill.unit, (uint32_t)fill.rows);
   uint32_t named = last - first < 32 ? ~0u << (last - first) : 0u;  // rows that are not to be filled
   const int64_t end = rows.begin[m + 1];
   for (int64_t at = find_key<false>(a.key, rows.begin[m], end, first); at < end; at += 32) {
@@ -509,10 +517,10 @@ int64_t chunks_of(const int64_t* row_begin, int n_workers, int chunk) {
   for (int m = 0; m < n_workers; ++m) n += ceil_div(row_begin[m + 1] - row_begin[m], chunk);
   return n;
 }
-// Short chunks where long ones would leave SMs without a warp in each
-// scheduler: a warp's loads of rows wait for one another.
+// Short chunks where long ones make fewer than 8 warps an SM: a warp's loads of
+// rows wait for one another.
 int chunk_pairs(int32_t cols, int n_workers, const int64_t* row_begin) {
-  return chunks_of(row_begin, n_workers, kLongChunk) * ceil_div(cols, kSlab) < 4 * (int64_t)current_sms() ? kShortChunk
+  return chunks_of(row_begin, n_workers, kLongChunk) * ceil_div(cols, kSlab) < 8 * (int64_t)current_sms() ? kShortChunk
                                                                                                       : kLongChunk;
 }
 BackwardLayout backward_layout(int32_t cols, int n_workers, const int64_t* row_begin) {
@@ -670,7 +678,10 @@ signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_wo
   a.vocab = (uint32_t)table_shape.rows, a.chunk = chunk, a.cols = cols, a.n_workers = n_workers, a.accumulate = accumulate != 0, a.scale = scale;
   a.slabs = (int32_t)ceil_div(cols, kSlab);
   const int64_t reduce_blocks = ceil_div(n_chunks, kReduceThreads / 32) * a.slabs;
-  const int64_t rest = ceil_div((int64_t)fill.rows - fill.head, 32) * n_workers;
+  // Up to 32 rows a warp, fewer while there are fewer than 32 warps an SM.
+  int64_t unit = ((int64_t)fill.rows - fill.head) * n_workers / (32 * current_sms());
+  fill.unit = (int32_t)(unit < 1 ? 1 : unit > 32 ? 32 : unit);
+  const int64_t rest = ceil_div((int64_t)fill.rows - fill.head, fill.unit) * n_workers;
   if (reduce_blocks + ceil_div(rest, kReduceThreads / 32) > INT32_MAX) return SIGNMUON_ERR_UNSUPPORTED;
   a.n_blocks = (int32_t)reduce_blocks;
   const unsigned blocks = (unsigned)(reduce_blocks + ceil_div(rest, kReduceThreads / 32));

@@ -5,7 +5,7 @@
 // and marshalling in Python took two to four times as long as a small
 // operator's kernels.
 #include <ATen/ATen.h>
-#include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -104,21 +104,27 @@ std::vector<int64_t> shares(int64_t rows, int64_t n_workers, const Splits& split
   return *splits;
 }
 
+// (Not by way of the dispatcher, which takes as long as the allocation.)
 Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, const Tensor& like) {
-  return at::empty(shape, at::TensorOptions(dtype).device(like.device()));
+  return Tensor(at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt));
 }
 
-// One tensor for each worker, each 16-byte aligned as the step wants them.
+// One tensor for each worker, each 16-byte aligned as the step wants them, in
+// one allocation.
 std::vector<Tensor> per_worker(int64_t n, at::IntArrayRef shape, at::ScalarType dtype, const Tensor& like) {
   int64_t elems = 1;
-  for (int64_t s : shape) elems *= s;
-  if (n == 1 || elems * (int64_t)c10::elementSize(dtype) % 16 == 0) {
-    std::vector<int64_t> whole = {n};
-    whole.insert(whole.end(), shape.begin(), shape.end());
-    return empty(whole, dtype, like).unbind(0);
+  std::vector<int64_t> strides(shape.size());
+  for (size_t d = shape.size(); d-- > 0;) strides[d] = elems, elems *= shape[d];
+  const int64_t granule = 16 / (int64_t)c10::elementSize(dtype), step = (elems + granule - 1) / granule * granule;
+  const Tensor whole = empty({n * step}, dtype, like);
+  std::vector<Tensor> out;
+  out.reserve(n);
+  for (int64_t i = 0; i < n; ++i) {
+    auto view = c10::make_intrusive<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()), whole.key_set(),
+                                                     whole.dtype());
+    view->set_sizes_and_strides(shape, strides, i * step);
+    out.emplace_back(std::move(view));
   }
-  std::vector<Tensor> out(n);
-  for (Tensor& t : out) t = empty(shape, dtype, like);
   return out;
 }
 std::vector<void*> pointers(const Tensor* t, size_t n) {
@@ -127,10 +133,8 @@ std::vector<void*> pointers(const Tensor* t, size_t n) {
   return p;
 }
 
-// The tensors' device and its current stream for the length of a call.  (No
-// autograd: it would follow the outputs' views.)
+// The tensors' device and its current stream for the length of a call.
 struct Call {
-  at::AutoDispatchBelowADInplaceOrView no_autograd;
   c10::cuda::OptionalCUDAGuard guard;
   void* stream;
   explicit Call(const Tensor& t) {
