@@ -61,6 +61,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __global__ void __launch_bounds__(kTeacherWarps * 32, 16)
 teacher_kernel(int64_t rows, int top, const void* __restrict__ ids, int wide, const void* __restrict__ logits, int bf16,
                int32_t vocab, float inv_t, int log_slots, Entry* __restrict__ entries, float* __restrict__ plogp, uint8_t* __restrict__ counts) {
+  allow_next_kernel();
   extern __shared__ Entry s_entries[];  // each warp: its entries, then its table of ids
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int64_t row = (int64_t)blockIdx.x * kTeacherWarps + warp;
@@ -298,6 +299,8 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
   __shared__ Soft s_soft[2][kMaxWarps], s_block[2][kMaxCluster];
   __shared__ float s_cross[kMaxWarps];
   __shared__ int s_n;
+  allow_next_kernel();
+  wait_for_kernel_before();
   const int threads = kThreads ? kThreads : blockDim.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = threads / 32;
   // Whole batches of every thread, and one more of what is left.
@@ -572,6 +575,8 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
   constexpr int kVec = RowSpan<T>::kVec;
   __shared__ Soft s_soft[kRowThreads / 32];
   __shared__ int s_n;
+  allow_next_kernel();
+  wait_for_kernel_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, n = a.vocab;
   const float c = a.inv_t * kLog2e;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -668,6 +673,7 @@ worker_loss_kernel(const float* __restrict__ row_loss, const uint8_t* __restrict
   __shared__ double s_sum[8];
   __shared__ int64_t s_n[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, m = blockIdx.x;
+  wait_for_kernel_before();
   double sum = 0.0;
   int64_t n = 0;
   for (int64_t i = workers.begin[m] + threadIdx.x; i < workers.begin[m + 1]; i += 256) sum += row_loss[i], n += counts[i];
@@ -692,7 +698,7 @@ int resident_clusters(cudaLaunchConfig_t cfg, int guess) {
   static thread_local Known known;
   const int dev = current_device(), ranks = (int)cfg.attrs[0].val.clusterDim.x, threads = (int)cfg.blockDim.x;
   if (known.dev != dev || known.ranks != ranks || known.threads != threads || known.smem != cfg.dynamicSmemBytes) {
-    cfg.gridDim = dim3((unsigned)ranks);
+    cfg.gridDim = dim3((unsigned)ranks), cfg.numAttrs = 1;  // the cluster alone
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, K, &cfg) != cudaSuccess || n < 1) n = guess < 1 ? 1 : guess;
     known.dev = dev, known.ranks = ranks, known.threads = threads, known.smem = cfg.dynamicSmemBytes, known.n = n;
@@ -730,10 +736,14 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)ranks, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr, cfg.numAttrs = ranks > 1 ? 1 : 0;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = (unsigned)ranks, attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_after does
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    // (A cluster that finds no place while the kernel before still holds SMs
+    // would be a second wave: 513 rows of 131101 fp32 174 us instead of 131.)
+    cfg.attrs = attrs, cfg.numAttrs = ranks > 1 ? 1 : 2;
     const int64_t room = kSmSmem / (smem + 2048), by_threads = 2 * most_threads / threads;
     int64_t an_sm = room < by_threads ? room : by_threads;
     an_sm = an_sm < 1 ? 1 : an_sm > 32 ? 32 : an_sm;
@@ -759,7 +769,7 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
     return;  // the caller asks for the error
   }
   const int64_t most = (int64_t)sms * 4;
-  rows_kernel<T><<<(unsigned)(a.rows < most ? a.rows : most), kRowThreads, 0, st>>>(a, workers);
+  launch_after(rows_kernel<T>, dim3((unsigned)(a.rows < most ? a.rows : most)), kRowThreads, 0, st, a, workers);
 }
 
 struct Layout {
@@ -827,7 +837,7 @@ signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_
     else launch_rows<__nv_bfloat16>(a, workers, cs);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
   }
-  worker_loss_kernel<<<n_workers, 256, 0, cs>>>(row_loss, a.counts, loss, workers);
+  launch_after(worker_loss_kernel, dim3((unsigned)n_workers), 256, 0, cs, row_loss, a.counts, loss, workers);
   return cuda_status(cudaGetLastError());
 }
 

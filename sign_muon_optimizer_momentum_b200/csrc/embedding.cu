@@ -119,6 +119,7 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
   uint16_t* s_count = s_tok + kTile;                                     // [kSortWarps][kDigits]
   __shared__ uint32_t s_digit[kDigits];  // first place of each digit
   __shared__ uint32_t s_warp[kSortWarps];
+  allow_next_kernel();
   const int n_tiles = tiles.begin[n_workers];
   if ((int)blockIdx.x >= n_tiles) {
     const int64_t t = (int64_t)(blockIdx.x - n_tiles) * kSortThreads + threadIdx.x;
@@ -175,14 +176,15 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
     // Counts to places: by digit, within a digit by warp.
     uint32_t total = 0;
     if (threadIdx.x < kDigits) {
+      // (Warps without pairs have counts that nobody reads.)
       for (int w0 = 0; w0 < used; w0 += 8) {
         uint32_t c[8];
 #pragma unroll
-        for (int w = 0; w < 8; ++w) c[w] = w0 + w < used ? s_count[(w0 + w) * kDigits + threadIdx.x] : 0;
+        for (int w = 0; w < 8; ++w) c[w] = s_count[(w0 + w) * kDigits + threadIdx.x];
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-          if (w0 + w < used) s_count[(w0 + w) * kDigits + threadIdx.x] = (uint16_t)total;
-          total += c[w];
+          s_count[(w0 + w) * kDigits + threadIdx.x] = (uint16_t)total;
+          total += w0 + w < used ? c[w] : 0;
         }
       }
     }
@@ -228,6 +230,8 @@ __global__ void __launch_bounds__(kMergeThreads)
 merge_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks blocks, int n_workers, int run,
              const uint32_t* __restrict__ key, const uint32_t* __restrict__ tok, uint32_t* __restrict__ out_key,
              uint32_t* __restrict__ out_tok) {
+  allow_next_kernel();
+  wait_for_kernel_before();
   const int m = worker_of_block(blocks, n_workers, blockIdx.x);
   const int n = (int)(rows.begin[m + 1] - rows.begin[m]);  // at most 2^31 - 1 tokens in all
   const int p = (blockIdx.x - blocks.begin[m]) * kMergeThreads + threadIdx.x;
@@ -374,6 +378,8 @@ __global__ void __launch_bounds__(kReduceThreads)
 reduce_kernel(const ReduceArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks chunks,
               const __grid_constant__ Fill fill) {
   constexpr int kVecs = kLaneCols / VEC, kBatch = 4;
+  allow_next_kernel();
+  wait_for_kernel_before();
   if ((int)blockIdx.x >= a.n_blocks) {
     fill_rest(a, rows, fill, (int64_t)(blockIdx.x - a.n_blocks) * (kReduceThreads / 32) + threadIdx.x / 32);
     return;
@@ -445,6 +451,7 @@ join_kernel(const ReduceArgs a, const __grid_constant__ WorkerRows rows, const _
   const int col0 = slab * kSlab + lane * VEC;
   int follow = 0, m = 0;
   uint32_t key = 0;
+  wait_for_kernel_before();
   if (chunk < chunks.begin[a.n_workers]) {
     m = worker_of_block(chunks, a.n_workers, chunk);
     const Chunk c = chunk_at(a, rows, chunks, m, chunk);
@@ -665,8 +672,8 @@ signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_wo
   int at = 0;
   for (int64_t run = kTile; run < longest; run *= kFan, at ^= 1) {
     const WorkerBlocks blocks = blocks_of(row_begin, n_workers, kMergeThreads);
-    merge_kernel<<<blocks.begin[n_workers], kMergeThreads, 0, cs>>>(rows, blocks, n_workers, (int)run, key[at], tok[at],
-                                                                    key[at ^ 1], tok[at ^ 1]);
+    launch_after(merge_kernel, dim3((unsigned)blocks.begin[n_workers]), kMergeThreads, 0, cs, rows, blocks, n_workers, (int)run,
+                 key[at], tok[at], key[at ^ 1], tok[at ^ 1]);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
   }
 
@@ -686,11 +693,12 @@ signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_wo
   a.n_blocks = (int32_t)reduce_blocks;
   const unsigned blocks = (unsigned)(reduce_blocks + ceil_div(rest, kReduceThreads / 32));
   by_types(dy_dtype, grad_dtype, vec, [&](auto td, auto tg, auto v) {
-    reduce_kernel<decltype(td), decltype(tg), decltype(v)::value><<<blocks, kReduceThreads, 0, cs>>>(a, rows, chunks, fill);
+    launch_after(reduce_kernel<decltype(td), decltype(tg), decltype(v)::value>, dim3(blocks), kReduceThreads, 0, cs, a, rows,
+                 chunks, fill);
     if ((e = cudaGetLastError()) != cudaSuccess) return;
-    join_kernel<decltype(tg), decltype(v)::value>
-        <<<dim3((unsigned)ceil_div(n_chunks, kJoinChunks), (unsigned)a.slabs), kJoinChunks * 32, 0, cs>>>(a, rows, chunks,
-                                                                                                       fill.grad);
+    launch_after(join_kernel<decltype(tg), decltype(v)::value>,
+                 dim3((unsigned)ceil_div(n_chunks, kJoinChunks), (unsigned)a.slabs), kJoinChunks * 32, 0, cs, a, rows, chunks,
+                 fill.grad);
     e = cudaGetLastError();
   });
   return cuda_status(e);

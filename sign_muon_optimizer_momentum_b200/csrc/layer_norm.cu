@@ -373,6 +373,7 @@ struct Backward {
 template <typename T, int VEC, int E, int kTpr, bool kWhole>
 __global__ void __launch_bounds__(kTpr > kThreads ? kTpr : kThreads)
 norm_backward_kernel(const NormArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks share) {
+  allow_next_kernel();
   using B = Backward<T, VEC, E, kTpr, kWhole>;
   using Sum = RowSum<kTpr, 2>;
   using Ring = typename B::Ring;
@@ -565,6 +566,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 norm_columns_kernel(const NormArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks share) {
   __shared__ float sh[2][8][32];
+  allow_next_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, cols = a.cols, col = blockIdx.y * 32 + lane;
   const int m = worker_of_block(share, a.n_workers, blockIdx.x);
   const int blocks = share.begin[m + 1] - share.begin[m];
@@ -597,6 +599,7 @@ norm_finalize_kernel(const float* part, int cols, int sums, int w_bf16, const __
   __shared__ float sh[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, col = blockIdx.x * 32 + lane;
   const int m = blockIdx.y, which = blockIdx.z;
+  wait_for_kernel_before();
   float s = 0.f;
   if (col < cols)
 #pragma unroll 4
@@ -819,8 +822,8 @@ signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const 
   });
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
-  norm_finalize_kernel<<<dim3((unsigned)ceil_div(cols, 32), (unsigned)n_workers, dbias ? 2u : 1u), 256, 0, cs>>>(
-      a.part, cols, dbias ? 2 : 1, a.w_bf16, share, dw, db);
+  launch_after(norm_finalize_kernel, dim3((unsigned)ceil_div(cols, 32), (unsigned)n_workers, dbias ? 2u : 1u), 256, 0, cs,
+               a.part, cols, dbias ? 2 : 1, a.w_bf16, share, dw, db);
   return cuda_status(cudaGetLastError());
 }
 

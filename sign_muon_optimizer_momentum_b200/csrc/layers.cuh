@@ -137,6 +137,13 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// A kernel that follows another one of the same call is launched while that
+// one still runs (launch_after), which hides the launch itself: the first
+// allows it when it starts, the second waits, before it reads or writes
+// anything, until the first is done and its writes are seen.
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // Host: a batch's rows by worker, as a kernel parameter.
 // ---------------------------------------------------------------------------
@@ -230,6 +237,18 @@ int resident_blocks(int threads, size_t smem) {
     slot.store(n, std::memory_order_relaxed);
   }
   return n;
+}
+
+// Launches a kernel that starts with wait_for_kernel_before().
+template <typename... P, typename... A>
+void launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid, cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);  // its error is cudaGetLastError's
 }
 
 }  // namespace signmuon
