@@ -698,7 +698,7 @@ int resident_clusters(cudaLaunchConfig_t cfg, int guess) {
   static thread_local Known known;
   const int dev = current_device(), ranks = (int)cfg.attrs[0].val.clusterDim.x, threads = (int)cfg.blockDim.x;
   if (known.dev != dev || known.ranks != ranks || known.threads != threads || known.smem != cfg.dynamicSmemBytes) {
-    cfg.gridDim = dim3((unsigned)ranks), cfg.numAttrs = 1;  // the cluster alone
+    cfg.gridDim = dim3((unsigned)ranks);
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, K, &cfg) != cudaSuccess || n < 1) n = guess < 1 ? 1 : guess;
     known.dev = dev, known.ranks = ranks, known.threads = threads, known.smem = cfg.dynamicSmemBytes, known.n = n;
@@ -736,14 +736,19 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = st;
-    cudaLaunchAttribute attrs[2];
-    attrs[0].id = cudaLaunchAttributeClusterDimension;
-    attrs[0].val.clusterDim.x = (unsigned)ranks, attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
-    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_after does
-    attrs[1].val.programmaticStreamSerializationAllowed = 1;
-    // (A cluster that finds no place while the kernel before still holds SMs
-    // would be a second wave: 513 rows of 131101 fp32 174 us instead of 131.)
-    cfg.attrs = attrs, cfg.numAttrs = ranks > 1 ? 1 : 2;
+    // A cluster, or a launch beside the kernel before (as launch_after's).  Not
+    // both: a cluster that finds no place while that one still holds SMs would
+    // be a second wave (513 rows of 131101 fp32: 174 us instead of 131).  And
+    // no clusters of one block (5208 rows of 193 fp32: 45 us instead of 29).
+    cudaLaunchAttribute attr;
+    if (ranks > 1) {
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = (unsigned)ranks, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    } else {
+      attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr.val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = &attr, cfg.numAttrs = 1;
     const int64_t room = kSmSmem / (smem + 2048), by_threads = 2 * most_threads / threads;
     int64_t an_sm = room < by_threads ? room : by_threads;
     an_sm = an_sm < 1 ? 1 : an_sm > 32 ? 32 : an_sm;
