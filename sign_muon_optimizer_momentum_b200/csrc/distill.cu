@@ -34,9 +34,6 @@ constexpr int kHeldThreads = 384, kHeldBatch = 3;
 constexpr int kStreamThreads = 512, kStreamBatch = 4;
 constexpr int kDepth = 3;                  // groups under way where a row is not held
 constexpr int kMaxCluster = 8;
-constexpr int kSplitThreads = 256;         // ... of a block that holds a part of it, at most
-constexpr int kRowBytes = 110 * 1024;      // of a row that two blocks an SM can hold each
-constexpr int kSliceBytes = 73 * 1024;     // of its parts, that three blocks an SM can hold
 constexpr int kSmSmem = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -711,26 +708,51 @@ template <typename T>
 void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
   constexpr int kVec = Chunk<T>::kVec;
   const int sms = current_sms();
-  // For the gradient a block holds a row, if two blocks an SM can, else the
-  // blocks of a cluster do, three an SM; more blocks, also for the losses, where
-  // rows are few.  (8192 rows of 50000 bf16: 336 us by blocks of 384 threads,
-  // 359 of 256, 393 of 512, 377 split in two; 513 rows of 131101 fp32: 120 us
-  // with three blocks an SM, 140 with two.)
+  // More blocks than rows where rows are few.
   const int shift = a.ld_z % kVec ? kVec - 1 : 0;
   const int64_t chunks = ((int64_t)a.vocab + shift + kVec - 1) / kVec;
-  const int batch = a.dz ? kHeldBatch : kStreamBatch, most_threads = a.dz ? kHeldThreads : kStreamThreads;
   int ranks = 1, threads = 0;
-  int64_t slice = 0, smem = 0;
-  for (;; ranks *= 2) {
-    const int most = ranks > 1 ? kSplitThreads : most_threads;
-    slice = ceil_div(chunks, ranks);
-    threads = (int)round_up((size_t)ceil_div(slice, batch), 32);
+  while (ranks < kMaxCluster && a.rows * ranks * 2 <= sms && chunks >= 1024 * ranks) ranks *= 2;
+  int64_t slice = 0, smem = 0, an_sm = 0;
+  const auto plan = [&](int r) {
+    const int batch = a.dz ? kHeldBatch : kStreamBatch, most = a.dz ? kHeldThreads : kStreamThreads;
+    slice = ceil_div(chunks, r);
+    const int64_t need = (int64_t)round_up((size_t)ceil_div(slice, batch), 32);
+    if (a.dz) {
+      // Blocks that an SM has shared memory and rows for (six, of long rows), and
+      // their share of its threads.
+      smem = slice * 16 + (int64_t)a.top * 4;
+      an_sm = kSmSmem / (smem + 2048);
+      const int64_t rows = ceil_div(a.rows * r, sms);
+      an_sm = an_sm > rows ? rows : an_sm;
+      an_sm = an_sm < 1 ? 1 : an_sm > 6 ? 6 : an_sm;
+      threads = (int)(2 * most / an_sm / 32 * 32);
+    } else {
+      threads = r > 1 ? 256 : most;
+    }
     if (threads > most) threads = most;
-    smem = (a.dz ? slice : (int64_t)kDepth * batch * threads) * 16 + (int64_t)a.top * 4;
-    if (ranks == kMaxCluster || !(smem > (ranks > 1 ? kSliceBytes : kRowBytes) ||
-                                  (a.rows * ranks * 2 <= sms && chunks >= 1024 * ranks)))
-      break;
+    if (need < threads) threads = (int)need;
+    if (!a.dz) smem = (int64_t)kDepth * batch * threads * 16 + (int64_t)a.top * 4;
+    const int64_t room = kSmSmem / (smem + 2048), by_threads = 2 * most / threads;
+    an_sm = room < by_threads ? room : by_threads;
+    an_sm = an_sm < 1 ? 1 : an_sm > 32 ? 32 : an_sm;
+  };
+  // For the gradient a cluster of such a size holds a row that the SMs' shared
+  // memory holds most of rows altogether, by two blocks an SM at least: that
+  // decides the time (1371 rows of 80288 bf16: 112 us with 160 KB of rows an SM,
+  // 133 with 120; 1000 of 131072: 126 with 197 KB, 147 with 131).
+  if (a.dz) {
+    int64_t most = -1;
+    int best = ranks;
+    for (int r = ranks; r <= kMaxCluster; r *= 2) {
+      plan(r);
+      if (smem + 2048 > kSmSmem) continue;
+      const int64_t rows_held = an_sm == 1 && slice * 16 > 64 * 1024 ? slice / 2 : an_sm * slice;
+      if (rows_held > most + most / 32) most = rows_held, best = r;
+    }
+    ranks = best;
   }
+  plan(ranks);
   const bool apart = a.dz && (!aligned_to(a.dz, 16) || a.ld_dz % kVec != a.ld_z % kVec);
   if (aligned_to(a.z, 16) && !apart && smem + 1024 <= kSmSmem) {
     cudaLaunchConfig_t cfg = {};
@@ -749,9 +771,6 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
       attr.val.programmaticStreamSerializationAllowed = 1;
     }
     cfg.attrs = &attr, cfg.numAttrs = 1;
-    const int64_t room = kSmSmem / (smem + 2048), by_threads = 2 * most_threads / threads;
-    int64_t an_sm = room < by_threads ? room : by_threads;
-    an_sm = an_sm < 1 ? 1 : an_sm > 32 ? 32 : an_sm;
     auto launch = [&](auto grad, auto block) {
       constexpr auto k = held_rows_kernel<T, decltype(grad)::value, decltype(block)::value>;
       resident_blocks<k>(32, 0);  // allows it the shared memory
@@ -764,9 +783,12 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
       cudaLaunchKernelEx(&cfg, k, a, workers, (int)slice);
     };
     auto by_block = [&](auto grad) {
+      // (Sizes that long rows get have kernels of their own.)
       constexpr int kMost = decltype(grad)::value ? kHeldThreads : kStreamThreads;
       if (threads == kMost) launch(grad, std::integral_constant<int, kMost>());
-      else if (threads == kSplitThreads) launch(grad, std::integral_constant<int, kSplitThreads>());
+      else if (threads == 256) launch(grad, std::integral_constant<int, 256>());
+      else if (threads == 192) launch(grad, std::integral_constant<int, 192>());
+      else if (threads == 128) launch(grad, std::integral_constant<int, 128>());
       else launch(grad, std::integral_constant<int, 0>());
     };
     if (a.dz) by_block(std::true_type());
