@@ -560,13 +560,12 @@ __global__ void __launch_bounds__(kWideThreads) norm_backward_wide_kernel(const 
   }
 }
 
-// ... and the column sums by blocks of 32 columns x 8 warps over the rows that
+// ... and, before it, the column sums by blocks of 32 columns x 8 warps over the rows that
 // a block of the other kernel would have had.
 template <typename T>
 __global__ void __launch_bounds__(256)
 norm_columns_kernel(const NormArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks share) {
   __shared__ float sh[2][8][32];
-  allow_next_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, cols = a.cols, col = blockIdx.y * 32 + lane;
   const int m = worker_of_block(share, a.n_workers, blockIdx.x);
   const int blocks = share.begin[m + 1] - share.begin[m];
@@ -702,10 +701,11 @@ void backward_launch(const NormArgs& a, const WorkerRows& rows, const int64_t* r
     return true;
   });
   if (!held) {
-    const int64_t most = (int64_t)sms * 4;
-    norm_backward_wide_kernel<T, kWhole ? VEC : 1><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
+    // The column sums first: dx may take dy's place.
     const int blocks = block_share(a.n_workers, row_begin, 64, sms, 1, share);
     norm_columns_kernel<T><<<dim3((unsigned)blocks, (unsigned)ceil_div(a.cols, 32)), 256, 0, st>>>(a, rows, *share);
+    const int64_t most = (int64_t)sms * 4;
+    norm_backward_wide_kernel<T, kWhole ? VEC : 1><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
   }
 }
 

@@ -392,7 +392,13 @@ def test_layer_norm_backward(cuda_lib, dtype, w_dtype, shares, cols, extra, bias
     again = layers.layer_norm_backward(dy, x, w, mean, rstd, len(shares), splits, bias=bias)
     assert torch.equal(again[0], dx) and all(torch.equal(p, q) for p, q in zip(again[1], dw))
     inplace = dy.clone()
-    layers.layer_norm_backward(inplace, x, w, mean, rstd, len(shares), splits, bias=bias, out=inplace)
+    _, dw2, db2 = layers.layer_norm_backward(inplace, x, w, mean, rstd, len(shares), splits, bias=bias, out=inplace)
+    for m, (a, b) in enumerate(zip(splits, splits[1:])):
+        t = D[a:b] * xh[a:b]
+        for got, want, mag in ((dw2[m], t.sum(0), t.abs().sum(0)), (db2[m], D[a:b].sum(0), D[a:b].abs().sum(0))) if bias else \
+                ((dw2[m], t.sum(0), t.abs().sum(0)),):
+            e = (b - a + 12) * U * mag
+            assert ((got.double() - want).abs() <= e + half(w_dtype) * (want.abs() + e)).all(), m
     e = r * (U * gy.abs() + e1 + xh.abs() * e2 + 4 * U * (gy.abs() + s1.abs() + (xh * s2).abs()) + e_xh * s2.abs())
     ref = r * (gy - s1 - xh * s2)
     assert ((inplace.double() - ref).abs() <= e + half(dtype) * (ref.abs() + e)).all()
