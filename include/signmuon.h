@@ -371,7 +371,7 @@ signmuon_status signmuon_embedding_forward(signmuon_shape table_shape, signmuon_
  * order.
  * dy: device [row_begin[n_workers], ld_dy] of dy_dtype; grad: host array of
  * n_workers device pointers, [rows, cols] of grad_dtype, row stride cols; no
- * two of them overlap.  At most 2^31 - 1 tokens.
+ * two of them overlap.  At most 2^30 tokens (else SIGNMUON_ERR_UNSUPPORTED).
  * workspace: device, >= signmuon_embedding_backward_workspace_bytes(...). */
 size_t signmuon_embedding_backward_workspace_bytes(signmuon_shape table_shape, int n_workers,
                                                    const int64_t* row_begin);
@@ -428,7 +428,8 @@ signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const 
  * 1 <= top <= 1024; row_loss: device fp32 [rows]; loss: device fp32
  * [n_workers]; dlogits: device [rows, ld_d] of dtype, NULL for the losses
  * alone (it may be logits itself, with the same stride).
- * temperature > 0 and finite.
+ * 1e-6 <= temperature <= 1e6; logits / temperature have to stay in fp32's
+ * range.  At most 2^30 rows, and 2^30 columns (else SIGNMUON_ERR_UNSUPPORTED).
  * workspace: device, >= signmuon_distill_workspace_bytes(...). */
 size_t signmuon_distill_workspace_bytes(int64_t rows, int top);
 signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_t* row_begin,

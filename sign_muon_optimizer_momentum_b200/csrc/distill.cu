@@ -17,8 +17,6 @@
 // The second one reads the logits and writes the gradient, each once, and is
 // bound by that: a block (for long rows a cluster of blocks) holds its row in
 // shared memory from the pass that sums to the pass that writes.
-#include <cmath>
-
 #include "layers.cuh"
 
 using namespace signmuon;
@@ -26,6 +24,7 @@ using namespace signmuon;
 namespace {
 
 constexpr int kMaxTop = 1024;
+constexpr int kMaxVocab = 1 << 30;   // columns of a row, and rows of a call: ints count them
 constexpr int kTeacherWarps = 4;
 constexpr int kRowThreads = 512;           // of a block that reads its row twice
 // Of a block that holds its rows (for the losses, that streams them) at most,
@@ -359,6 +358,7 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
           for (int i = max(col, 0); i < min(col + kVec, a.vocab); ++i) store_elem(dz, i, sizeof(T) == 2, 0.f);
         }
       }
+      __syncwarp();
     }
   };
 
@@ -697,7 +697,8 @@ int resident_clusters(cudaLaunchConfig_t cfg, int guess) {
   if (known.dev != dev || known.ranks != ranks || known.threads != threads || known.smem != cfg.dynamicSmemBytes) {
     cfg.gridDim = dim3((unsigned)ranks);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, K, &cfg) != cudaSuccess || n < 1) n = guess < 1 ? 1 : guess;
+    if (cudaOccupancyMaxActiveClusters(&n, K, &cfg) != cudaSuccess) cudaGetLastError(), n = 0;
+    if (n < 1) n = guess < 1 ? 1 : guess;
     known.dev = dev, known.ranks = ranks, known.threads = threads, known.smem = cfg.dynamicSmemBytes, known.n = n;
   }
   return known.n;
@@ -816,7 +817,7 @@ Layout layout_of(int64_t rows, int top) {
 extern "C" {
 
 size_t signmuon_distill_workspace_bytes(int64_t rows, int top) {
-  return rows < 0 || top < 1 || top > kMaxTop ? 0 : layout_of(rows, top).total;
+  return rows < 0 || rows > kMaxVocab || top < 1 || top > kMaxTop ? 0 : layout_of(rows, top).total;
 }
 
 signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_t* row_begin, signmuon_dtype dtype,
@@ -826,9 +827,10 @@ signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_
                                       void* workspace, size_t ws_bytes, void* stream) {
   if (vocab <= 0 || n_workers <= 0 || n_workers > SIGNMUON_MAX_WORKERS || !row_begin ||
       !valid_splits(row_begin, n_workers, row_begin[n_workers]) || !known_dtype(dtype) || !known_dtype(top_dtype) || top < 1 ||
-      top > kMaxTop || ld < vocab || (dlogits && ld_d < vocab) || !loss || !(temperature > 0.f) || std::isinf(temperature))
+      top > kMaxTop || ld < vocab || (dlogits && ld_d < vocab) || !loss || !(temperature >= 1e-6f && temperature <= 1e6f))
     return SIGNMUON_ERR_INVALID_ARG;
   const int64_t n = row_begin[n_workers];
+  if (vocab > kMaxVocab || n > kMaxVocab) return SIGNMUON_ERR_UNSUPPORTED;
   if (n > 0 && (!logits || !top_ids || !top_logits || !row_loss)) return SIGNMUON_ERR_INVALID_ARG;
   const int zb = dtype_bytes(dtype);
   if (!aligned_to(logits, zb) || !aligned_to(dlogits, zb) || !aligned_to(top_ids, ids_int64 ? 8 : 4) ||
@@ -838,7 +840,6 @@ signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_
   const signmuon_status st = check_ws(workspace, ws_bytes, l.total);
   if (st) return st;
   const int64_t teacher_blocks = ceil_div(n, kTeacherWarps);
-  if (teacher_blocks > INT32_MAX) return SIGNMUON_ERR_UNSUPPORTED;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   RowArgs a = {};

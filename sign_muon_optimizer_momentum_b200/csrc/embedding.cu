@@ -29,6 +29,7 @@ using namespace signmuon;
 
 namespace {
 
+constexpr int64_t kMaxTokens = 1 << 30;  // of a backward call: places among them are ints
 constexpr int kLookupThreads = 256;
 constexpr int kLookupVecs = 4;       // vectors a lane loads of a row
 constexpr int kSortThreads = 1024;
@@ -233,7 +234,7 @@ merge_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ Wo
   allow_next_kernel();
   wait_for_kernel_before();
   const int m = worker_of_block(blocks, n_workers, blockIdx.x);
-  const int n = (int)(rows.begin[m + 1] - rows.begin[m]);  // at most 2^31 - 1 tokens in all
+  const int n = (int)(rows.begin[m + 1] - rows.begin[m]);  // at most kMaxTokens in all
   const int p = (blockIdx.x - blocks.begin[m]) * kMergeThreads + threadIdx.x;
   if (p >= n) return;
   key += rows.begin[m];
@@ -607,7 +608,7 @@ static bool valid_backward_shape(signmuon_shape s, int n_workers, const int64_t*
 }
 
 size_t signmuon_embedding_backward_workspace_bytes(signmuon_shape table_shape, int n_workers, const int64_t* row_begin) {
-  if (!valid_backward_shape(table_shape, n_workers, row_begin) || row_begin[n_workers] > INT32_MAX) return 0;
+  if (!valid_backward_shape(table_shape, n_workers, row_begin) || row_begin[n_workers] > kMaxTokens) return 0;
   return backward_layout(table_shape.cols, n_workers, row_begin).total;
 }
 
@@ -620,7 +621,7 @@ signmuon_status signmuon_embedding_backward(signmuon_shape table_shape, int n_wo
       !grad || ld_dy < cols)
     return SIGNMUON_ERR_INVALID_ARG;
   const int64_t n = row_begin[n_workers];
-  if (cols > kMaxCols || n > INT32_MAX) return SIGNMUON_ERR_UNSUPPORTED;
+  if (cols > kMaxCols || n > kMaxTokens) return SIGNMUON_ERR_UNSUPPORTED;
   if (n > 0 && (!ids || !dy)) return SIGNMUON_ERR_INVALID_ARG;
   if (!aligned_to(ids, ids_int64 ? 8 : 4) || !aligned_to(dy, dtype_bytes(dy_dtype))) return SIGNMUON_ERR_ALIGNMENT;
   Fill fill = {};

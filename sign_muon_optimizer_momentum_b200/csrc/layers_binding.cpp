@@ -5,11 +5,13 @@
 // and marshalling in Python took two to four times as long as a small
 // operator's kernels.
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <algorithm>
 #include <optional>
 #include <string>
 #include <tuple>
@@ -79,6 +81,14 @@ int64_t check_out(const Tensor& t, at::IntArrayRef shape, at::ScalarType dtype, 
   check_type(t, dtype, what);
   TORCH_CHECK_VALUE(t.sizes() == shape, what, ": expected shape ", shape, ", got ", t.sizes());
   return rows_of(t, what).ld;
+}
+
+// An output shares no memory with an input; or, where that is allowed, it is
+// the same tensor.  (Of tensors with gaps between their rows this cannot be
+// told: they may be columns of one buffer.)
+void check_apart(const Tensor& out, const Tensor& in, const char* what, bool same = false) {
+  const at::MemOverlapStatus s = at::get_overlap_status(out, in);
+  TORCH_CHECK_VALUE(s != at::MemOverlapStatus::Partial && (same || s != at::MemOverlapStatus::Full), "out overlaps ", what);
 }
 
 bool check_ids(const Tensor& ids, const char* what, const Tensor& like) {
@@ -162,6 +172,7 @@ Tensor embedding_forward(const Tensor& table, const Tensor& ids, double scale, s
   std::vector<int64_t> shape = ids.sizes().vec();
   shape.push_back(t.cols);
   const int64_t ld = out ? check_out(*out, shape, type, "out", table) : t.cols;
+  if (out) check_apart(*out, table, "table"), check_apart(*out, ids, "ids");
   const Call call(table);
   const Tensor y = out ? *out : empty(shape, type, table);
   check_status("signmuon_embedding_forward",
@@ -188,7 +199,13 @@ std::vector<Tensor> embedding_backward(const Tensor& ids, const Tensor& grad_out
       const std::string what = "out[" + std::to_string(m) + "]";
       check_out((*out)[m], {vocab, dy.cols}, type, what.c_str(), grad_out);
       TORCH_CHECK_VALUE((*out)[m].is_contiguous(), what, " must be contiguous");
+      check_apart((*out)[m], grad_out, "grad_out"), check_apart((*out)[m], ids, "ids");
     }
+    std::vector<const char*> at;
+    for (const Tensor& t : *out) at.push_back(static_cast<const char*>(t.data_ptr()));
+    std::sort(at.begin(), at.end());
+    for (size_t m = 1; m < at.size(); ++m)
+      TORCH_CHECK_VALUE(at[m] - at[m - 1] >= (ptrdiff_t)(*out)[0].nbytes(), "gradient buffers overlap");
   } else {
     TORCH_CHECK_VALUE(!accumulate, "accumulate needs out");
   }
@@ -223,6 +240,8 @@ std::tuple<Tensor, Tensor, Tensor> layer_norm_forward(const Tensor& x, const Ten
   const signmuon_dtype code = dtype_code(x.scalar_type()), w_code = dtype_code(weight.scalar_type());
   const signmuon_shape shape = shape_of(1, r.cols);
   const int64_t ld = out ? check_out(*out, x.sizes(), x.scalar_type(), "out", x) : r.cols;
+  if (out) check_apart(*out, x, "x", true), check_apart(*out, weight, "weight");
+  if (out && bias) check_apart(*out, *bias, "bias");
   const Call call(x);
   const Tensor y = out ? *out : empty(x.sizes(), x.scalar_type(), x);
   const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
@@ -253,6 +272,11 @@ std::tuple<Tensor, std::vector<Tensor>, std::optional<std::vector<Tensor>>> laye
   const signmuon_shape shape = shape_of(1, r.cols);
   const std::vector<int64_t> rows = shares(r.n, n_workers, splits);
   const int64_t ld = out ? check_out(*out, x.sizes(), x.scalar_type(), "out", x) : r.cols;
+  if (out) {
+    check_apart(*out, grad_out, "grad_out", true);
+    for (const auto& [t, what] : {std::pair<const Tensor&, const char*>(x, "x"), {weight, "weight"}, {mean, "mean"}, {rstd, "rstd"}})
+      check_apart(*out, t, what);
+  }
   const Call call(x);
   const Tensor dx = out ? *out : empty(x.sizes(), x.scalar_type(), x);
   std::vector<Tensor> dw = per_worker(n_workers * (bias ? 2 : 1), weight.sizes(), weight.scalar_type(), x);
@@ -285,12 +309,15 @@ std::tuple<Tensor, Tensor, MaybeTensor> distill(const Tensor& logits, const Tens
   const int64_t top = top_ids.size(-1);
   TORCH_CHECK_VALUE(top >= 1 && top <= 1024, "between 1 and 1024 top logits are supported");
   TORCH_CHECK_VALUE(top_logits.is_contiguous(), "top_logits must be contiguous");
-  TORCH_CHECK_VALUE(temperature > 0 && temperature < std::numeric_limits<double>::infinity(),
-                    "temperature must be positive and finite");
+  TORCH_CHECK_VALUE(temperature >= 1e-6 && temperature <= 1e6, "temperature must be in [1e-6, 1e6]");
   const signmuon_dtype code = dtype_code(logits.scalar_type()), top_code = dtype_code(top_logits.scalar_type());
   const signmuon_shape shape = shape_of(1, z.cols);
   const std::vector<int64_t> rows = shares(z.n, n_workers, splits);
   const int64_t ld = with_grad && out ? check_out(*out, logits.sizes(), logits.scalar_type(), "out", logits) : z.cols;
+  if (with_grad && out) {
+    check_apart(*out, logits, "logits", true);
+    check_apart(*out, top_ids, "top_ids"), check_apart(*out, top_logits, "top_logits");
+  }
   const Call call(logits);
   const Tensor loss = empty({n_workers}, at::kFloat, logits), row_loss = empty(lead, at::kFloat, logits);
   MaybeTensor dz;

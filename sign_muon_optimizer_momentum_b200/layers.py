@@ -107,7 +107,7 @@ def distill_loss(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: torch.
     logits.shape[:-1], and loss[m] the mean over worker m's rows, fp32
     [n_workers].
 
-    logits: rows of the vocabulary; top_ids (int32 or int64), top_logits:
+    temperature: in [1e-6, 1e6].  logits: rows of the vocabulary; top_ids (int32 or int64), top_logits:
     contiguous rows of 1 to 1024 entries; an entry with an id outside the
     vocabulary or a logit of -inf is absent, and a row without entries is
     ignored (loss 0, not counted in the mean)."""

@@ -65,7 +65,7 @@ def test_embedding_refusals(lib):
     assert bwd(ddt=2) == 1 and bwd(gdt=2) == 1
     assert bwd(ids=P + 4) == 2 and bwd(dy=ODD) == 2 and bwd(grad=(P, ODD)) == 2 and bwd(ws=P + 16) == 2
     assert bwd(ws=0) == 4 and bwd(nbytes=512) == 4
-    assert bwd(rows=(0, 2, 1 << 31)) == 3
+    assert bwd(rows=(0, 2, (1 << 30) + 1)) == 3
     size = L.signmuon_embedding_backward_workspace_bytes
     assert size((10, 8), [0, 3, 2]) == 0 and size((0, 8), [0, 3]) == 0 and size((10, 8), [0, 0]) >= 256
     assert size((10, 8), [0, 40]) >= 256 + 4 * 4 * 40 + 2 * 2 * 8 * 4
@@ -103,8 +103,9 @@ def test_distill_refusals(lib):
     assert f(vocab=0) == 1 and f(rows=(0, 4, 2)) == 1 and f(dt=2) == 1 and f(tdt=2) == 1 and f(z=0) == 1 and f(ld=7) == 1
     assert f(top=0) == 1 and f(top=1025) == 1 and f(ids=0) == 1 and f(tl=0) == 1 and f(loss=0) == 1 and f(row=0) == 1
     assert f(ldd=7) == 1
-    for t in (0.0, -1.0, math.inf, math.nan):
+    for t in (0.0, -1.0, math.inf, math.nan, 1e-7, 1e7):
         assert f(temp=t) == 1
+    assert f(vocab=(1 << 30) + 1, ld=1 << 31, ldd=1 << 31) == 3 and f(rows=(0, (1 << 30) + 1)) == 3
     assert f(z=ODD) == 2 and f(dz=ODD) == 2 and f(ids=P + 4) == 2 and f(tl=ODD) == 2 and f(loss=P + 2) == 2 and f(ws=P + 16) == 2
     assert f(ws=0) == 4 and f(nbytes=300) == 4
     assert L.signmuon_distill_workspace_bytes(4, 0) == 0 and L.signmuon_distill_workspace_bytes(-1, 2) == 0
@@ -661,6 +662,14 @@ def test_refused_tensors(cuda_lib):
         (ValueError, lambda: layers.embedding_backward(ids, x, 4, n_workers=2, out=[x])),
         (ValueError, lambda: layers.embedding_backward(ids, x, 4, out=[torch.zeros(8, 4, device="cuda").t()])),
         (ValueError, lambda: layers.embedding_backward(ids, x, 0)),
+        (ValueError, lambda: layers.embedding_backward(ids, x, 2, n_workers=2, out=[x[:2], x[1:3]])),
+        (ValueError, lambda: layers.embedding_backward(ids, x, 2, n_workers=2, out=[x[:2], x[:2]])),
+        (ValueError, lambda: layers.embedding_forward(x, ids, out=x)),
+        (ValueError, lambda: layers.embedding_backward(ids, x, 4, out=[x])),
+        (ValueError, lambda: layers.layer_norm_forward(x[:3], w, out=x[1:])),
+        (ValueError, lambda: layers.layer_norm_backward(x[:3], x[:3].clone(), w, w[:3], w[:3], out=x[1:])),
+        (ValueError, lambda: layers.layer_norm_backward(x.clone(), x, w, w[:4], w[:4], out=x)),
+        (ValueError, lambda: layers.distill_loss_and_grad(x[:3], top[:3], u[:3], out=x[1:])),
         (ValueError, lambda: layers.layer_norm_forward(x, w[:7])),
         (TypeError, lambda: layers.layer_norm_forward(x, w, w.bfloat16())),
         (ValueError, lambda: layers.layer_norm_forward(x, w, eps=-1.0)),
