@@ -14,7 +14,7 @@
 //             latency and takes few SMs, the fill is bound by HBM.
 //   2. merge  Only for workers of more than one tile: each pair's place is its
 //             place in its own run plus the smaller pairs of the other runs,
-//             found by binary search, kFan runs at a time.
+//             found by search, kFan runs at a time.
 //   3. reduce A warp takes a chunk of consecutive sorted pairs (32, or 8 where
 //             that leaves SMs without work) and a slab of columns, adds the rows of each run of equal ids in registers and
 //             writes the runs that lie within the chunk.  What a run that
@@ -39,10 +39,8 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 constexpr int64_t kFillBeside = 40 << 20;  // bytes that are filled in the time of a sort
-// Runs merged at a time: as many as a thread searches side by side.  (100003
-// tokens: 5 us for tiles of 4096 and 11 for each of two merges; tiles of 16384
-// took 33, and one merge of 32 runs 31.)
-constexpr int kFan = 8;
+constexpr int kFan = 32;             // runs merged at a time (one lane each)
+constexpr int kMergeStage = 11264;   // keys of other runs that a block of the merge holds
 constexpr int kMergeThreads = 256;
 constexpr int kLongChunk = 32, kShortChunk = 8;  // sorted pairs a warp of the reduction takes
 constexpr int kLaneCols = 8;         // columns of a lane's slab
@@ -226,46 +224,122 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
 
 // ------------------------------------------------------------------ merge
 // Runs of `run` sorted pairs of each worker, kFan at a time, to runs of
-// kFan * run (run is a power of two).  Equal keys keep the runs' order.
+// kFan * run (run is kTile times a power of kFan).  Equal keys keep the runs'
+// order.  A block has kMergeThreads pairs of one run, so what it looks for in
+// another run lies between the places of its first and its last key there.
+// Those are found first, by warps of 32 probes at a time, and the keys between
+// them brought into shared memory, if they fit: the threads' searches then wait
+// for no load.  (100003 tokens: 15 us for 25 runs, where two merges of eight
+// runs each, searched in L2 from end to end, took 11 us each.)
 __global__ void __launch_bounds__(kMergeThreads)
 merge_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks blocks, int n_workers, int run,
              const uint32_t* __restrict__ key, const uint32_t* __restrict__ tok, uint32_t* __restrict__ out_key,
              uint32_t* __restrict__ out_tok) {
+  constexpr int kWarps = kMergeThreads / 32, kSearches = 2 * kFan / kWarps, kSide = 8;
+  __shared__ uint32_t s_key[kMergeStage];
+  // Of each run: the places of the block's first and behind its last key, from
+  // the run's start; where the keys between are in s_key.
+  __shared__ int s_edge[2 * kFan], s_at[kFan + 1];
   allow_next_kernel();
   wait_for_kernel_before();
   const int m = worker_of_block(blocks, n_workers, blockIdx.x);
   const int n = (int)(rows.begin[m + 1] - rows.begin[m]);  // at most kMaxTokens in all
-  const int p = (blockIdx.x - blocks.begin[m]) * kMergeThreads + threadIdx.x;
-  if (p >= n) return;
+  const int p0 = (blockIdx.x - blocks.begin[m]) * kMergeThreads, p = p0 + threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   key += rows.begin[m];
-  const uint32_t k = key[p];
-  const int mine = p / run, group = mine / kFan * kFan, own = mine - group;
+  const int mine = p0 / run, group = mine / kFan * kFan, own = mine - group;
   const int runs = min(kFan, (n + run - 1) / run - group);
-  // Pairs of the other runs that go before: keys below k, and equal ones of
-  // an earlier run.  The searches go side by side, without branches: one alone
-  // would wait for each of its loads.
-  int at[kFan];
+  const uint32_t edge[2] = {key[p0], key[min(p0 + kMergeThreads, n) - 1]}, k = p < n ? key[p] : edge[1];
+  const uint32_t t = p < n ? tok[rows.begin[m] + p] : 0;
+  // What goes before a pair: keys below its own, and in earlier runs equal ones.
+  int at[kSearches];
 #pragma unroll
-  for (int i = 0; i < kFan; ++i) at[i] = 0;
-  for (int step = run; step; step /= 2) {
-    uint32_t seen[kFan];
+  for (int q = 0; q < kSearches; ++q) at[q] = 0;
+  int step = run;
+  do {
+    step = (step + 31) / 32;
+    uint32_t seen[kSearches];
 #pragma unroll
-    for (int i = 0; i < kFan; ++i) {
-      const int begin = (group + min(i, runs - 1)) * run;
-      seen[i] = key[begin + min(at[i] + step, min(run, n - begin)) - 1];
+    for (int q = 0; q < kSearches; ++q) {
+      const int i = (warp * kSearches + q) / 2;
+      seen[q] = ~0u;
+      if (i < runs && i != own) {
+        const int begin = (group + i) * run, probe = at[q] + (lane + 1) * step;
+        if (probe <= min(run, n - begin)) seen[q] = key[begin + probe - 1];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kFan; ++i) {
-      const int begin = (group + min(i, runs - 1)) * run, probe = at[i] + step;
-      at[i] = probe <= min(run, n - begin) && seen[i] < k + (i < own ? 1u : 0u) ? probe : at[i];
+    for (int q = 0; q < kSearches; ++q) {
+      const int i = (warp * kSearches + q) / 2;
+      at[q] += __popc(__ballot_sync(0xffffffffu, seen[q] < edge[q % 2] + (i < own ? 1u : 0u))) * step;
     }
+  } while (step > 1);
+  if (lane == 0)
+#pragma unroll
+    for (int q = 0; q < kSearches; ++q) s_edge[warp * kSearches + q] = at[q];
+  __syncthreads();
+  if (warp == 0) {
+    int scan = s_edge[2 * lane + 1] - s_edge[2 * lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    s_at[lane + 1] = scan;
+    if (lane == 0) s_at[0] = 0;
   }
+  __syncthreads();
+  // kSide searches side by side, without branches: one alone would wait for
+  // each of its loads.
   int before = 0;
+  auto search = [&](int i0, int i1, int first, auto in_shared) {
+    for (; i0 < i1; i0 += kSide) {
+      const uint32_t* from[kSide];
+      int len[kSide], to[kSide], most = 0;
 #pragma unroll
-  for (int i = 0; i < kFan; ++i) before += i < runs && i != own ? at[i] : 0;
-  const int64_t place = rows.begin[m] + (int64_t)group * run + (p - mine * run) + before;
-  out_key[place] = k;
-  out_tok[place] = tok[rows.begin[m] + p];
+      for (int q = 0; q < kSide; ++q) {
+        const int i = i0 + q;
+        len[q] = s_at[i + 1] - s_at[i], to[q] = 0;
+        if constexpr (decltype(in_shared)::value) from[q] = s_key + (s_at[i] - s_at[first]);
+        else from[q] = key + (group + min(i, runs - 1)) * run + s_edge[2 * i];
+        before += s_edge[2 * i];
+        most = max(most, len[q]);
+      }
+      for (int s = most ? 1 << (31 - __clz(most)) : 0; s; s /= 2) {
+#pragma unroll
+        for (int q = 0; q < kSide; ++q) {
+          const int probe = to[q] + s;
+          if (probe <= len[q] && from[q][probe - 1] < k + (i0 + q < own ? 1u : 0u)) to[q] = probe;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kSide; ++q) before += to[q];
+    }
+  };
+  // As many runs at a time, in kSides, as s_key holds.
+  for (int first = 0, last; first < runs; first = last) {
+    for (last = first; last < runs && s_at[last + kSide] - s_at[first] <= kMergeStage;) last += kSide;
+    if (last == first) {
+      last += kSide;
+      search(first, last, first, std::false_type());
+      continue;
+    }
+    __syncthreads();
+    for (int i = first + warp; i < min(last, runs); i += kWarps) {
+      const uint32_t* from = key + (group + i) * run + s_edge[2 * i];
+      uint32_t* to = s_key + (s_at[i] - s_at[first]);
+      const int len = s_at[i + 1] - s_at[i];
+#pragma unroll 8
+      for (int j = lane; j < len; j += 32) to[j] = from[j];
+    }
+    __syncthreads();
+    search(first, last, first, std::true_type());
+  }
+  if (p < n) {
+    const int64_t place = rows.begin[m] + (int64_t)group * run + (p - mine * run) + before;
+    out_key[place] = k;
+    out_tok[place] = t;
+  }
 }
 
 // ----------------------------------------------------------------- reduce

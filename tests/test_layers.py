@@ -191,6 +191,8 @@ def token_ids(g, n, vocab, kind, dtype=torch.int64):
         ids = torch.where(at, far[torch.randint(0, 4, (n,), generator=g, device="cuda")], ids)
         if dtype == torch.int64 and n > 2:
             ids[n // 2] = 1 << 40
+    if kind == "dense":  # but for the first 4096, few ids
+        ids[4096:] %= 1 + vocab // 1000
     if kind == "none":
         ids = torch.full((n,), -1, device="cuda")
     return ids.to(dtype)
@@ -246,8 +248,9 @@ EMBED_BACKWARD = [
     ([4096], 513, 40, "uniform", 0),
     ([4097, 12289], 60000, 24, "zipf", 0),
     ([20000], 3, 17, "uniform", 1),
-    ([40000], 70000, 8, "zipf", 0),             # more than eight sorted tiles: two merges
-    ([270000, 7], 263000, 4, "zipf", 0),        # more than 64: three
+    ([40000], 70000, 8, "zipf", 0),             # ten sorted tiles: a merge
+    ([270000, 7], 263000, 4, "zipf", 0),        # more than 32: two
+    ([130000, 9000], 60000, 4, "dense", 0),     # what a block looks through does not fit shared memory
     ([9000], 1, 300, "same", 0),
     ([700] * 9, 128, 770, "zipf", 0),
 ]
