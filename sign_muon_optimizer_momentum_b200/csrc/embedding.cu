@@ -32,6 +32,7 @@ namespace {
 constexpr int64_t kMaxTokens = 1 << 30;  // of a backward call: places among them are ints
 constexpr int kLookupThreads = 256;
 constexpr int kLookupVecs = 4;       // vectors a lane loads of a row
+constexpr int kAnyVecs = 4;          // the same, of a row at any address
 constexpr int kSortThreads = 1024;
 constexpr int kSortItems = 4;        // pairs a thread
 constexpr int kTile = kSortThreads * kSortItems;
@@ -51,7 +52,8 @@ constexpr int kLongRun = 16;         // chunks from which a whole block adds a r
 
 // ----------------------------------------------------------------- lookup
 // lanes (a power of two) lanes take kLookupVecs vectors each of a token's
-// row; blockIdx.y is the segment of rows that are longer than that.
+// row; blockIdx.y is the segment of rows that are longer than that.  Bound by
+// memory: 32768 tokens of 4096 bf16 from 50000 rows in 61 us (floor 54).
 template <typename TW, typename TY, int VEC>
 __global__ void __launch_bounds__(kLookupThreads)
 lookup_kernel(const TW* __restrict__ table, int64_t ld_table, int32_t vocab, int32_t cols, int64_t n_tokens,
@@ -80,6 +82,84 @@ lookup_kernel(const TW* __restrict__ table, int64_t ld_table, int32_t vocab, int
       // to put together.
       if (VEC * sizeof(TY) >= 8) store_stream<TY, VEC>(y + token * ld_y + col, v);
       else store_vec<TY, VEC>(y + token * ld_y + col, v);
+    }
+  }
+}
+
+// Rows of one type that are not all on 16 bytes.  y is written in whole 16
+// bytes where they lie in the row; what goes there starts at the same place
+// within 16 bytes all along a row of the table, so each is cut from two aligned
+// vectors, by one shift that a row's lanes share.  Lanes with four vectors each
+// (32 KB of loads under way an SM) are worth more than more warps with two.
+// 65536 tokens of 1001 columns: bf16 42 us, fp32 83 us, where element by element
+// they took 120 and 117 (1000 columns: 34 and 63); 131072 tokens of 33: 12 and 10
+// for 26 and 25.
+template <typename T>
+__global__ void __launch_bounds__(kLookupThreads, 5)
+lookup_any_kernel(const T* __restrict__ table, int64_t ld_table, int32_t vocab, int32_t cols, int64_t n_tokens,
+                  const void* __restrict__ ids, int wide, float scale, T* __restrict__ y, int64_t ld_y, int lanes) {
+  constexpr int kVec = 16 / sizeof(T), kWord = 4 / sizeof(T);  // elements of 16 bytes, and of 4
+  const int64_t token = (int64_t)blockIdx.x * (kLookupThreads / lanes) + threadIdx.x / lanes;
+  if (token >= n_tokens) return;
+  const int64_t id = load_id(ids, token, wide);
+  const bool in = id >= 0 && id < vocab;
+  const T* src = table + (in ? id : 0) * ld_table;
+  T* dst = y + token * ld_y;
+  const int shift = (int)(reinterpret_cast<uintptr_t>(dst) % 16 / sizeof(T));  // of y's first vector before the row
+  const int off = (int)((reinterpret_cast<uintptr_t>(src) / sizeof(T) - shift) % kVec);  // in the table's vectors
+  const int first = blockIdx.y * lanes * kAnyVecs + threadIdx.x % lanes;
+  const uint4* from = reinterpret_cast<const uint4*>(src - shift - off) + first;
+  T* to = dst - shift + first * kVec;
+  int col = first * kVec - shift;
+  // The table's first and last rows, where a vector may reach over its ends.
+  if (in && (id * ld_table < 2 * kVec || (vocab - 1 - id) * ld_table < 2 * kVec)) {
+    for (int i = 0; i < kAnyVecs; ++i, col += lanes * kVec)
+      for (int j = max(col, 0); j < min(col + kVec, cols); ++j)
+        store_elem(dst, j, sizeof(T) == 2, load_elem(src, j, sizeof(T) == 2) * scale);
+    return;
+  }
+  uint4 a[kAnyVecs], b[kAnyVecs];
+#pragma unroll
+  for (int i = 0; i < kAnyVecs; ++i) {
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (in && col + i * lanes * kVec < cols) {
+      a[i] = __ldg(from + i * lanes);
+      if (off) b[i] = __ldg(from + i * lanes + 1);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kAnyVecs; ++i, col += lanes * kVec, to += lanes * kVec) {
+    if (col >= cols) break;
+    uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
+    const int words = off / kWord;
+    if (words & 2)
+#pragma unroll
+      for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+    if (words & 1)
+#pragma unroll
+      for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+    if (off % kWord)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+    if (scale != 1.f) {
+      typename RawVec<T, kVec>::type raw;
+      memcpy(&raw, w, 16);
+      float v[kVec];
+      unpack(raw, v);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[j] = in ? v[j] * scale : 0.f;
+      pack(v, raw);
+      memcpy(w, &raw, 16);
+    }
+    if (col >= 0 && col + kVec <= cols) {
+      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (col + j >= 0 && col + j < cols) {
+          if (sizeof(T) == 4) reinterpret_cast<uint32_t*>(to)[j] = w[j];
+          else reinterpret_cast<uint16_t*>(to)[j] = (uint16_t)(w[j / kWord] >> j % kWord * 16);
+        }
     }
   }
 }
@@ -661,17 +741,34 @@ signmuon_status signmuon_embedding_forward(signmuon_shape table_shape, signmuon_
   if (!aligned_to(table, dtype_bytes(table_dtype)) || !aligned_to(y, dtype_bytes(y_dtype)) || !aligned_to(ids, ids_int64 ? 8 : 4))
     return SIGNMUON_ERR_ALIGNMENT;
   const int vec = common_width(table_dtype, table, ld_table, y_dtype, y, ld_y, cols);
+  const int full = 16 / dtype_bytes(y_dtype);
+  const bool any = table_dtype == y_dtype && vec < full;
+  const int64_t vecs = any ? ceil_div(cols + full - 1, full) : ceil_div(cols, vec);  // of a row at most
   int lanes = 1;
-  while (lanes < 32 && lanes * vec < cols) lanes *= 2;
+  while (lanes < 32 && lanes * (any ? kAnyVecs : 1) < vecs) lanes *= 2;
   const int64_t blocks = ceil_div(n_tokens, kLookupThreads / lanes);
-  const int segments = (int)ceil_div(cols, (int64_t)lanes * vec * kLookupVecs);
+  const int segments = (int)ceil_div(vecs, (int64_t)lanes * (any ? kAnyVecs : kLookupVecs));
   if (blocks > INT32_MAX) return SIGNMUON_ERR_UNSUPPORTED;
   if (!n_tokens) return SIGNMUON_OK;
+  if (any) {
+    auto launch = [&](auto t) {
+      using T = decltype(t);
+      lookup_any_kernel<T><<<dim3((unsigned)blocks, (unsigned)segments), kLookupThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+          static_cast<const T*>(table), ld_table, table_shape.rows, cols, n_tokens, ids, ids_int64 != 0, scale,
+          static_cast<T*>(y), ld_y, lanes);
+    };
+    if (table_dtype == SIGNMUON_F32) launch(float());
+    else launch(__nv_bfloat16());
+    return cuda_status(cudaGetLastError());
+  }
   by_types(table_dtype, y_dtype, vec, [&](auto tw, auto ty, auto v) {
-    lookup_kernel<decltype(tw), decltype(ty), decltype(v)::value>
-        <<<dim3((unsigned)blocks, (unsigned)segments), kLookupThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-            static_cast<const decltype(tw)*>(table), ld_table, table_shape.rows, cols, n_tokens, ids, ids_int64 != 0, scale,
-            static_cast<decltype(ty)*>(y), ld_y, lanes);
+    using TW = decltype(tw);
+    using TY = decltype(ty);
+    constexpr int kVec = decltype(v)::value;
+    if constexpr (!std::is_same_v<TW, TY> || kVec * sizeof(TW) == 16)
+      lookup_kernel<TW, TY, kVec><<<dim3((unsigned)blocks, (unsigned)segments), kLookupThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+          static_cast<const TW*>(table), ld_table, table_shape.rows, cols, n_tokens, ids, ids_int64 != 0, scale,
+          static_cast<TY*>(y), ld_y, lanes);
   });
   return cuda_status(cudaGetLastError());
 }

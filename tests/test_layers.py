@@ -221,6 +221,29 @@ def test_embedding_forward(cuda_lib, table_dtype, dtype, n, vocab, cols, extra, 
     assert ((y.double() - ref).abs() <= ref.abs() * (U + half(dtype) * (1 + U))).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,ld", [(1, 1), (3, 3), (7, 9), (8, 8), (17, 17), (33, 34), (130, 131), (515, 515), (1026, 1026)])
+def test_embedding_forward_any_address(cuda_lib, dtype, cols, ld):
+    """Tables and outputs at every place within 16 bytes, and rows up to the
+    ends of their buffers: what lies around them is left as it was."""
+    g = gen(cols)
+    vocab, n, per = 23, 41, 16 // dtype.itemsize
+    ids = token_ids(g, n, vocab, "padded")
+    ids[:4] = torch.tensor([0, vocab - 1, 1, vocab - 2], device="cuda")
+    inside = (ids >= 0) & (ids < vocab)
+    for a in range(per):
+        for b in range(per):
+            table = normal(g, a + (vocab - 1) * ld + cols, dtype=dtype)[a:].as_strided((vocab, cols), (ld, 1))
+            buf = torch.full((b + n * ld + 16,), 7.0, dtype=dtype, device="cuda")
+            out = buf[b:].as_strided((n, cols), (ld, 1))
+            want = buf.clone()
+            for scale in (1.0, -0.5):
+                want[b:].as_strided((n, cols), (ld, 1)).copy_(torch.where(inside[:, None], table[ids.where(inside, 0)] * scale, 0.0))
+                layers.embedding_forward(table, ids, scale=scale, out=out)
+                assert torch.equal(buf, want), (a, b, scale)
+
+
 def embedding_reference(ids, dy, vocab, splits, scale):
     """Gradients and the sums of their terms' magnitudes, and counts."""
     out = []
