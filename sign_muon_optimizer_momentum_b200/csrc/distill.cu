@@ -54,77 +54,100 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // ---------------------------------------------------------------- teacher
-__global__ void __launch_bounds__(kTeacherWarps * 32, 16)
+// A warp a row, kPer entries a lane in registers.  Bound by the latency of its
+// steps, one after the other (2048 rows of 64 entries: 4.1 us, 8192: 6.6; with
+// a table of ids filled by atomicCAS, which takes the lanes one by one, 9.7 and
+// 12.5).
+template <int kPer>
+__global__ void __launch_bounds__(kTeacherWarps * 32)
 teacher_kernel(int64_t rows, int top, const void* __restrict__ ids, int wide, const void* __restrict__ logits, int bf16,
-               int32_t vocab, float inv_t, int log_slots, Entry* __restrict__ entries, float* __restrict__ plogp, uint8_t* __restrict__ counts) {
+               int32_t vocab, float inv_t, Entry* __restrict__ entries, float* __restrict__ plogp, uint8_t* __restrict__ counts) {
+  // Each warp: the ids, and a hash table of twice as many slots, to see whether
+  // one comes twice; then, if one does, the entries.
+  constexpr int kSlots = 64 * kPer;
+  extern __shared__ Entry s_entries[];
   allow_next_kernel();
-  extern __shared__ Entry s_entries[];  // each warp: its entries, then its table of ids
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int64_t row = (int64_t)blockIdx.x * kTeacherWarps + warp;
   if (row >= rows) return;
-  Entry* mine = s_entries + warp * top;
-  int32_t* table = reinterpret_cast<int32_t*>(s_entries + kTeacherWarps * top) + (warp << log_slots);
-  for (int i = lane; i < 1 << log_slots; i += 32) table[i] = -1;
-  __syncwarp();
-  float top_u = -INFINITY;
-  bool any = false, bad = false, twice = false;
-#pragma unroll 4
-  for (int k = lane; k < top; k += 32) {
-    const int64_t id = load_id(ids, row * top + k, wide);
-    const float u = load_elem(logits, row * top + k, bf16);
-    mine[k] = {id >= 0 && id < vocab && u != -INFINITY ? (int32_t)id : -1, u};
-  }
-  for (int k = lane; k < top; k += 32) {
-    const Entry e = mine[k];
-    if (e.id < 0) continue;
-    top_u = fmaxf(top_u, e.p), any = true, bad |= e.p != e.p;
-    // Ids in a hash table of at least twice as many slots, to see whether one
-    // comes twice.
-    for (uint32_t at = (uint32_t)e.id * 2654435769u >> (32 - log_slots);; at = (at + 1) & ((1u << log_slots) - 1)) {
-      const int32_t seen = atomicCAS(&table[at], -1, e.id);
-      twice |= seen == e.id;
-      if (seen == -1 || seen == e.id) break;
+  Entry* mine = s_entries + warp * (32 * kPer);
+  int32_t* s_id = reinterpret_cast<int32_t*>(mine);
+  uint16_t* table = reinterpret_cast<uint16_t*>(s_id + 32 * kPer);
+  int32_t id[kPer];
+  float x[kPer], e[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int k = lane + 32 * j;
+    id[j] = -1, x[j] = -INFINITY;
+    if (k < top) {
+      const int64_t v = load_id(ids, row * top + k, wide);
+      x[j] = load_elem(logits, row * top + k, bf16);
+      if (v >= 0 && v < vocab && x[j] != -INFINITY) id[j] = (int32_t)v;
     }
   }
-  twice = __any_sync(0xffffffffu, twice);
+  bool any = false, bad = false, twice = false;
+  float top_u = -INFINITY;
+  uint32_t open = 0;  // entries that are to be compared still
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    s_id[lane + 32 * j] = id[j];
+    if (id[j] >= 0) top_u = fmaxf(top_u, x[j]), any = true, bad |= x[j] != x[j], open |= 1u << j;
+  }
+  // In turns: each writes itself into its id's slot.  One stays there, and is
+  // done; one that finds another entry of its id there comes twice; the others
+  // (with them, all of an id or none) try another hash.
+  for (uint32_t odd = 2654435769u; __any_sync(0xffffffffu, open); odd *= 0x2c1b3c6du) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (open >> j & 1) table[(uint32_t)id[j] * odd >> 16 & (kSlots - 1)] = (uint16_t)(lane + 32 * j);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (open >> j & 1) {
+        const int there = table[(uint32_t)id[j] * odd >> 16 & (kSlots - 1)];
+        if (s_id[there] == id[j]) open &= ~(1u << j), twice |= there != lane + 32 * j;
+      }
+    __syncwarp();
+  }
   any = __any_sync(0xffffffffu, any);
   // fmaxf drops a NaN: one among the entries makes the row NaN.
   top_u = __any_sync(0xffffffffu, bad) ? NAN : warp_max(top_u);
   float sum = 0.f;
-  for (int k = lane; k < top; k += 32)
-    if (mine[k].id >= 0) sum += expf((mine[k].p - top_u) * inv_t);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    x[j] = (x[j] - top_u) * inv_t;
+    e[j] = id[j] >= 0 ? expf(x[j]) : 0.f;
+    sum += e[j];
+  }
   sum = warp_sum(sum);
   const float log_sum = logf(sum), inv_sum = 1.f / sum;
   float h = 0.f;
-  for (int k = lane; k < top; k += 32)
-    if (mine[k].id >= 0) {
-      const float x = (mine[k].p - top_u) * inv_t, p = expf(x) * inv_sum;
-      if (p != 0.f) h = fmaf(p, x - log_sum, h);
-      mine[k].p = p;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (id[j] >= 0) {
+      e[j] *= inv_sum;
+      if (e[j] != 0.f) h = fmaf(e[j], x[j] - log_sum, h);
     }
   h = warp_sum(h);
-  __syncwarp();
-  // The first entry of an id holds all of the id's.
-  for (int k = lane; k < top; k += 32) {
-    Entry e = mine[k];
-    if (e.id >= 0 && !twice) {
-      if (e.p == 0.f) e.id = -1;
-    } else if (e.id >= 0) {
-      float p = 0.f;
-      bool first = true;
-      for (int j = 0; j < top; ++j) {
-        const Entry o = mine[j];
-        if (o.id == e.id) {
-          p += o.p;
-          first &= j >= k;
-        }
-      }
-      e.id = first && p != 0.f ? e.id : -1;
-      e.p = p;
-    }
-    entries[row * top + k] = e;
-  }
   if (lane == 0) plogp[row] = h, counts[row] = any;
+  if (!__any_sync(0xffffffffu, twice)) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (lane + 32 * j < top) entries[row * top + lane + 32 * j] = {e[j] != 0.f ? id[j] : -1, e[j]};
+    return;
+  }
+  // The first entry of an id holds all of the id's.
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) mine[lane + 32 * j] = {id[j], e[j]};
+  __syncwarp();
+  for (int k = lane; k < top; k += 32) {
+    const int32_t v = mine[k].id;
+    float p = 0.f;
+    bool first = true;
+    for (int i = 0; i < top; ++i)
+      if (mine[i].id == v) p += mine[i].p, first &= i >= k;
+    entries[row * top + k] = {v >= 0 && first && p != 0.f ? v : -1, p};
+  }
 }
 
 // ------------------------------------------------------------------- rows
@@ -852,13 +875,20 @@ signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_
   WorkerRows workers = {};
   for (int m = 0; m <= n_workers; ++m) workers.begin[m] = row_begin[m];
   if (n) {
-    int log_slots = 5;
-    while ((1 << log_slots) < 2 * top) ++log_slots;
-    resident_blocks<teacher_kernel>(kTeacherWarps * 32, 0);  // allows it the shared memory
-    teacher_kernel<<<(unsigned)teacher_blocks, kTeacherWarps * 32,
-                     kTeacherWarps * (top * sizeof(Entry) + (sizeof(int32_t) << log_slots)), cs>>>(
-        n, top, top_ids, ids_int64 != 0, top_logits, top_dtype == SIGNMUON_BF16, vocab, a.inv_t, log_slots,
-        reinterpret_cast<Entry*>(ws + l.entries), reinterpret_cast<float*>(ws + l.plogp), ws + l.counts);
+    auto teacher = [&](auto per) {
+      constexpr int kPer = decltype(per)::value;
+      constexpr size_t kSmem = kTeacherWarps * 32 * kPer * sizeof(Entry);
+      resident_blocks<teacher_kernel<kPer>>(kTeacherWarps * 32, kSmem);  // allows it the shared memory
+      teacher_kernel<kPer><<<(unsigned)teacher_blocks, kTeacherWarps * 32, kSmem, cs>>>(
+          n, top, top_ids, ids_int64 != 0, top_logits, top_dtype == SIGNMUON_BF16, vocab, a.inv_t,
+          reinterpret_cast<Entry*>(ws + l.entries), reinterpret_cast<float*>(ws + l.plogp), ws + l.counts);
+    };
+    if (top <= 32) teacher(std::integral_constant<int, 1>());
+    else if (top <= 64) teacher(std::integral_constant<int, 2>());
+    else if (top <= 128) teacher(std::integral_constant<int, 4>());
+    else if (top <= 256) teacher(std::integral_constant<int, 8>());
+    else if (top <= 512) teacher(std::integral_constant<int, 16>());
+    else teacher(std::integral_constant<int, 32>());
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_status(e);
     if (dtype == SIGNMUON_F32) launch_rows<float>(a, workers, cs);
