@@ -31,6 +31,7 @@ constexpr int kRowThreads = 512;           // of a block that reads its row twic
 // and the chunks that a thread copies as one group.
 constexpr int kHeldThreads = 384, kHeldBatch = 3;
 constexpr int kStreamThreads = 512, kStreamBatch = 4;
+constexpr int kShortWarps = 8, kShortCols = 1024;  // of a block of short rows; columns of one at most
 constexpr int kDepth = 3;                  // groups under way where a row is not held
 constexpr int kMaxCluster = 8;
 constexpr int kSmSmem = 227 * 1024;
@@ -193,6 +194,120 @@ __device__ __forceinline__ Soft warp_join(Soft a) {
 // log q of a logit.
 __device__ __forceinline__ float soft_log(Soft a, float z, float c) {
   return (fmaf(z, c, -a.e) - log2f(a.s)) * 0.6931471805599453f;
+}
+
+// Thread t's share, of `threads`, of the rows [begin, end) that count, 16 bytes at a time
+// (counts starts on 16 bytes and has room to the next).
+__device__ __forceinline__ int count_rows(const uint8_t* counts, int64_t begin, int64_t end, int t, int threads) {
+  int n = 0;
+#pragma unroll 4
+  for (int64_t at = begin / 16 * 16 + t * 16; at < end; at += threads * 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(counts + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (at >= begin && at + 16 <= end) {
+      n += __popc(w[0] | w[1] << 1 | w[2] << 2 | w[3] << 3);  // each byte is 0 or 1
+    } else {
+      for (int i = max((int)(begin - at), 0); i < min((int)(end - at), 16); ++i) n += counts[at + i];
+    }
+  }
+  return n;
+}
+
+// ------------------------------------------------------------- short rows
+// A warp a row, kE elements a lane in registers: one exponential an element, and
+// no barrier a row.  (5927 rows of 586 bf16 with their gradient: 20 us, where a block
+// a row, as below, took 33; 20000 rows of 193 fp32: 28 for 67 us.)
+template <typename T, bool kGrad, int kE>
+__global__ void __launch_bounds__(kShortWarps * 32)
+short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, int per_warp) {
+  // The teacher's part of the gradient by column, zero but for a row's entries.
+  __shared__ float s_sub[kGrad ? kShortWarps : 1][kGrad ? 32 * kE : 1];
+  allow_next_kernel();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, n = a.vocab;
+  const float c = a.inv_t * kLog2e;
+  const int64_t first = ((int64_t)blockIdx.x * kShortWarps + warp) * per_warp;
+  const int64_t last = first + per_warp < a.rows ? first + per_warp : a.rows;
+  float* sub = s_sub[kGrad ? warp : 0];
+  if constexpr (kGrad)
+#pragma unroll
+    for (int i = 0; i < kE; ++i) sub[lane + 32 * i] = 0.f;
+  wait_for_kernel_before();
+  // The rows that count of the worker that the block's first row belongs to.
+  __shared__ int s_n;
+  int worker = -1, first_worker = 0;
+  if constexpr (kGrad) {
+    const int64_t block_row = (int64_t)blockIdx.x * kShortWarps * per_warp;
+    while (workers.begin[first_worker + 1] <= block_row) ++first_worker;
+    if (threadIdx.x == 0) s_n = 0;
+    __syncthreads();
+    const int rows = __reduce_add_sync(0xffffffffu, count_rows(a.counts, workers.begin[first_worker], workers.begin[first_worker + 1],
+                                                               threadIdx.x, kShortWarps * 32));
+    if (lane == 0) atomicAdd(&s_n, rows);
+    __syncthreads();
+  }
+  float scale = 0.f;
+  for (int64_t row = first; row < last; ++row) {
+    const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
+    T* dz = kGrad ? static_cast<T*>(a.dz) + row * a.ld_dz : nullptr;
+    if (!a.counts[row]) {
+      if (lane == 0) a.row_loss[row] = 0.f;
+      if constexpr (kGrad)
+#pragma unroll
+        for (int i = 0; i < kE; ++i)
+          if (lane + 32 * i < n) store_elem(dz, lane + 32 * i, sizeof(T) == 2, 0.f);
+      continue;
+    }
+    float v[kE];
+#pragma unroll
+    for (int i = 0; i < kE; ++i) v[i] = lane + 32 * i < n ? load_elem(z, lane + 32 * i, sizeof(T) == 2) : -INFINITY;
+    if constexpr (kGrad)
+      if (worker < 0 || workers.begin[worker + 1] <= row) {
+        while (workers.begin[++worker + 1] <= row) {}
+        int rows = s_n;
+        if (worker != first_worker)
+          rows = __reduce_add_sync(0xffffffffu, count_rows(a.counts, workers.begin[worker], workers.begin[worker + 1], lane, 32));
+        scale = a.grad_scale * a.t / (float)rows;
+      }
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < kE; ++i) top = fmaxf(top, v[i]);
+    top = warp_max(top);
+    const float e = ceilf(top * c), ref = soft_ref(e);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) v[i] = exp2_fast(fmaf(v[i], c, ref)), s += v[i];
+    const Soft soft = {e, warp_sum(s)};
+    // The entries, with their logits before the gradient may take their place.
+    const Entry* entries = a.entries + row * a.top;
+    float cross = 0.f;
+    for (int k0 = lane; k0 < a.top; k0 += 128) {
+      Entry entry[4];
+      float logit[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) entry[j] = k0 + 32 * j < a.top ? entries[k0 + 32 * j] : Entry{-1, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) logit[j] = entry[j].id >= 0 ? load_elem(z, entry[j].id, sizeof(T) == 2) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (entry[j].id >= 0) {
+          cross = fmaf(entry[j].p, soft_log(soft, logit[j], c), cross);
+          if constexpr (kGrad) sub[entry[j].id] = entry[j].p * scale;
+        }
+    }
+    cross = warp_sum(cross);
+    if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - cross);
+    if constexpr (kGrad) {
+      const float qs = scale / soft.s;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const int col = lane + 32 * i;
+        if (col < n) store_elem(dz, col, sizeof(T) == 2, fmaf(v[i], qs, -sub[col]));
+        sub[col] = 0.f;
+      }
+      __syncwarp();
+    }
+  }
 }
 
 // --------------------------------------------------- rows in shared memory
@@ -415,8 +530,14 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
     float logit = 0.f;
     if (entry.id >= 0) logit = load_elem(a.z, row * a.ld_z + entry.id, sizeof(T) == 2);
     entry_next = row_next < a.rows && (int)threadIdx.x < a.top ? a.entries[row_next * a.top + threadIdx.x] : none;
-    for (int k = threadIdx.x + threads; k < a.top; k += threads)
-      if (entries[k].id >= 0) entry_z[k] = load_elem(a.z, row * a.ld_z + entries[k].id, sizeof(T) == 2);
+    for (int k0 = threadIdx.x + threads; k0 < a.top; k0 += 4 * threads) {
+      int id[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) id[i] = k0 + i * threads < a.top ? entries[k0 + i * threads].id : -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (id[i] >= 0) entry_z[k0 + i * threads] = load_elem(a.z, row * a.ld_z + id[i], sizeof(T) == 2);
+    }
     const float plogp = threadIdx.x == 0 ? a.plogp[row] : 0.f;
 
     Soft soft = {-INFINITY, 0.f};
@@ -500,9 +621,7 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
       if (worker < 0 || workers.begin[worker + 1] <= row) {
         // The rows that count of this row's worker.
         while (workers.begin[++worker + 1] <= row) {}
-        int n = 0;
-        for (int64_t i = workers.begin[worker] + threadIdx.x; i < workers.begin[worker + 1]; i += threads) n += a.counts[i];
-        n = __reduce_add_sync(0xffffffffu, n);
+        const int n = __reduce_add_sync(0xffffffffu, count_rows(a.counts, workers.begin[worker], workers.begin[worker + 1], threadIdx.x, threads));
         if (threadIdx.x == 0) s_n = 0;
         __syncthreads();
         if (lane == 0) atomicAdd(&s_n, n);
@@ -647,9 +766,7 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
     // The rows of this worker that count.
     int m = 0;
     while (workers.begin[m + 1] <= row) ++m;
-    int cnt = 0;
-    for (int64_t i = workers.begin[m] + threadIdx.x; i < workers.begin[m + 1]; i += kRowThreads) cnt += a.counts[i];
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    const int cnt = __reduce_add_sync(0xffffffffu, count_rows(a.counts, workers.begin[m], workers.begin[m + 1], threadIdx.x, kRowThreads));
     if (lane == 0) atomicAdd(&s_n, cnt);
     __syncthreads();
     const float scale = a.grad_scale * a.t / (float)s_n, qs = scale / soft.s, ref = soft_ref(soft.e);
@@ -732,6 +849,24 @@ template <typename T>
 void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
   constexpr int kVec = Chunk<T>::kVec;
   const int sms = current_sms();
+  if (a.vocab <= kShortCols) {
+    auto launch = [&](auto grad, auto per_lane) {
+      constexpr auto k = short_rows_kernel<T, decltype(grad)::value, decltype(per_lane)::value>;
+      const int64_t most = (int64_t)sms * resident_blocks<k>(kShortWarps * 32, 0) * kShortWarps;
+      const int per_warp = (int)ceil_div(a.rows, most);
+      launch_after(k, dim3((unsigned)ceil_div(a.rows, (int64_t)per_warp * kShortWarps)), kShortWarps * 32, 0, st, a, workers,
+                   per_warp);
+    };
+    auto by_length = [&](auto grad) {
+      if (a.vocab <= 128) launch(grad, std::integral_constant<int, 4>());
+      else if (a.vocab <= 256) launch(grad, std::integral_constant<int, 8>());
+      else if (a.vocab <= 512) launch(grad, std::integral_constant<int, 16>());
+      else launch(grad, std::integral_constant<int, 32>());
+    };
+    if (a.dz) by_length(std::true_type());
+    else by_length(std::false_type());
+    return;  // the caller asks for the error
+  }
   // More blocks than rows where rows are few.
   const int shift = a.ld_z % kVec ? kVec - 1 : 0;
   const int64_t chunks = ((int64_t)a.vocab + shift + kVec - 1) / kVec;
@@ -752,7 +887,17 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
       an_sm = an_sm < 1 ? 1 : an_sm > 6 ? 6 : an_sm;
       threads = (int)(2 * most / an_sm / 32 * 32);
     } else {
-      threads = r > 1 ? 256 : most;
+      // Fewer threads a row, and more rows at a time, unless that leaves more SMs
+      // without a row at the end: each row costs its bytes and the time of 64 KB
+      // more (2048 rows of 50000, 128 or 512 threads: bf16 53 and 65 us, fp32 75
+      // and 72; 924 of 13205 bf16: 16 and 26).
+      threads = 256;
+      int64_t least = INT64_MAX;
+      for (int t = most; r == 1 && t >= 128; t /= 2) {
+        const int64_t at_once = 2 * most / t, rounds = ceil_div(a.rows, at_once * sms);
+        const int64_t cost = rounds * (at_once * chunks * 16 + 65536);
+        if (cost < least) least = cost, threads = t;
+      }
     }
     if (threads > most) threads = most;
     if (need < threads) threads = (int)need;

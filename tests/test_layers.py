@@ -7,6 +7,7 @@ Bounds.  u = 2^-24 is the most an fp32 rounding is off, relative to the value;
 terms taken one after another in fp32 is off by at most n u times the sum of
 the terms' magnitudes.
 """
+import itertools
 import math
 
 import pytest
@@ -548,6 +549,10 @@ DISTILL = [  # rows by worker, vocab, top, kind, extra columns
     ([4, 4], 1001, 20, "holes", 0), ([6], 4096, 33, "holes", 8), ([3], 32001, 8, "plain", 0), ([2, 3], 50000, 64, "holes", 0),
     ([3], 50001, 128, "holes", 3), ([2], 131101, 20, "plain", 0), ([2], 300, 1024, "twice", 0), ([2, 2], 60000, 1000, "plain", 0),
     ([300, 100], 200, 16, "holes", 0), ([0], 50, 4, "plain", 0), ([2], 200000, 7, "holes", 1), ([400], 3001, 40, "plain", 0),
+    # A warp a row, several rows a warp, workers that begin within a block; and
+    # the shortest rows that blocks take.
+    ([20000, 0, 37, 5], 33, 3, "holes", 0), ([9], 129, 40, "twice", 1), ([40, 3], 1024, 70, "holes", 0),
+    ([30, 2], 1025, 300, "holes", 0), ([17, 31, 250], 1500, 5, "holes", 0), ([1500], 5000, 6, "holes", 0),
 ]
 
 
@@ -580,8 +585,8 @@ def test_distill(cuda_lib, dtype, top_dtype, shares, vocab, top, kind, extra, te
 @pytest.mark.gpu
 def test_distill_extreme_logits(cuda_lib):
     """Finite masks of the type's lowest value, large logits, and what is not finite."""
-    for dtype in (F32, BF16):
-        z, ids, u, splits = distill_inputs([6], 3000, 8, dtype, "plain")
+    for dtype, vocab in itertools.product((F32, BF16), (300, 3000)):
+        z, ids, u, splits = distill_inputs([6], vocab, 8, dtype, "plain")
         lowest = torch.finfo(dtype).min
         z[0, 100:] = lowest
         ids[0] = torch.arange(8, device="cuda")
@@ -591,18 +596,18 @@ def test_distill_extreme_logits(cuda_lib):
         u[4, 1:] = -1e30
         check_distill(z, ids, u, splits, 1.0, 8)
         check_distill(z, ids, u, splits, 0.5, 8)
-    z[1, 5], z[2, 5], u[3, 2] = float("nan"), float("inf"), float("nan")
-    z[4] = float("-inf")
-    clean = [0, 5]
-    ref = layers.distill_loss_and_grad(z[clean].contiguous(), ids[clean].contiguous(), u[clean].contiguous())
-    _, row, dz = layers.distill_loss_and_grad(z, ids, u)
-    assert row[1:5].isnan().all() and dz[1:5].isnan().any(1).all()
-    assert torch.equal(row[clean], ref[1])
-    # A present entry whose student logit is -inf: the loss is inf, the gradient finite.
-    z, ids, u, _ = distill_inputs([1], 3000, 8, F32, "plain")
-    z[0, ids[0, 2]] = float("-inf")
-    loss, row, dz = layers.distill_loss_and_grad(z, ids, u)
-    assert row[0] == math.inf and loss[0] == math.inf and dz.isfinite().all()
+        z[1, 5], z[2, 5], u[3, 2] = float("nan"), float("inf"), float("nan")
+        z[4] = float("-inf")
+        clean = [0, 5]
+        ref = layers.distill_loss_and_grad(z[clean].contiguous(), ids[clean].contiguous(), u[clean].contiguous())
+        _, row, dz = layers.distill_loss_and_grad(z, ids, u)
+        assert row[1:5].isnan().all() and dz[1:5].isnan().any(1).all()
+        assert torch.equal(row[clean], ref[1])
+        # A present entry whose student logit is -inf: the loss is inf, the gradient finite.
+        z, ids, u, _ = distill_inputs([1], vocab, 8, F32, "plain")
+        z[0, ids[0, 2]] = float("-inf")
+        loss, row, dz = layers.distill_loss_and_grad(z, ids, u)
+        assert row[0] == math.inf and loss[0] == math.inf and dz.isfinite().all()
 
 
 @pytest.mark.gpu
