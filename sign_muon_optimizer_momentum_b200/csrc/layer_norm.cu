@@ -560,33 +560,39 @@ __global__ void __launch_bounds__(kWideThreads) norm_backward_wide_kernel(const 
   }
 }
 
-// ... and, before it, the column sums by blocks of 32 columns x 8 warps over the rows that
-// a block of the other kernel would have had.
-template <typename T>
+// ... and, before it, the column sums by blocks of 32 x VEC columns x 8 warps over
+// the rows that a block of the other kernel would have had.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
 norm_columns_kernel(const NormArgs a, const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks share) {
-  __shared__ float sh[2][8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, cols = a.cols, col = blockIdx.y * 32 + lane;
+  __shared__ float sh[2][8][VEC][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, cols = a.cols, col = (blockIdx.y * 32 + lane) * VEC;
   const int m = worker_of_block(share, a.n_workers, blockIdx.x);
   const int blocks = share.begin[m + 1] - share.begin[m];
-  float dw = 0.f, db = 0.f;
+  const int64_t step = (int64_t)blocks * 8, end = rows.begin[m + 1];
+  const T* x = static_cast<const T*>(a.x) + col;
+  const T* dy = static_cast<const T*>(a.dy) + col;
+  float dw[VEC] = {}, db[VEC] = {};
   if (col < cols)
-    for (int64_t row = rows.begin[m] + (int64_t)(blockIdx.x - share.begin[m]) * 8 + warp; row < rows.begin[m + 1];
-         row += (int64_t)blocks * 8) {
-      float u[1], g[1];
-      unpack(*reinterpret_cast<const typename RawVec<T, 1>::type*>(static_cast<const T*>(a.x) + row * a.ld_x + col), u);
-      unpack(*reinterpret_cast<const typename RawVec<T, 1>::type*>(static_cast<const T*>(a.dy) + row * a.ld_dy + col), g);
-      db += g[0];
-      dw = fmaf(g[0], (u[0] - a.mean[row]) * a.rstd[row], dw);
+#pragma unroll 4
+    for (int64_t row = rows.begin[m] + (int64_t)(blockIdx.x - share.begin[m]) * 8 + warp; row < end; row += step) {
+      float u[VEC], g[VEC];
+      unpack(*reinterpret_cast<const typename RawVec<T, VEC>::type*>(x + row * a.ld_x), u);
+      unpack(*reinterpret_cast<const typename RawVec<T, VEC>::type*>(dy + row * a.ld_dy), g);
+      const float mean = a.mean[row], r = a.rstd[row];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) db[j] += g[j], dw[j] = fmaf(g[j], (u[j] - mean) * r, dw[j]);
     }
-  sh[0][warp][lane] = dw;
-  sh[1][warp][lane] = db;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) sh[0][warp][j][lane] = dw[j], sh[1][warp][j][lane] = db[j];
   __syncthreads();
   const int sums = a.has_bias ? 2 : 1;
-  if (warp < sums && col < cols) {
+  for (int i = threadIdx.x; i < sums * 32 * VEC; i += 256) {
+    const int which = i / (32 * VEC), c = i % (32 * VEC), at = blockIdx.y * 32 * VEC + c;
+    if (at >= cols) continue;
     float s = 0.f;
-    for (int i = 0; i < 8; ++i) s += sh[warp][i][lane];
-    a.part[((int64_t)blockIdx.x * sums + warp) * cols + col] = s;
+    for (int w = 0; w < 8; ++w) s += sh[which][w][c % VEC][c / VEC];
+    a.part[((int64_t)blockIdx.x * sums + which) * cols + at] = s;
   }
 }
 
@@ -702,10 +708,11 @@ void backward_launch(const NormArgs& a, const WorkerRows& rows, const int64_t* r
   });
   if (!held) {
     // The column sums first: dx may take dy's place.
+    constexpr int kVec = kWhole ? VEC : 1;
     const int blocks = block_share(a.n_workers, row_begin, 64, sms, 1, share);
-    norm_columns_kernel<T><<<dim3((unsigned)blocks, (unsigned)ceil_div(a.cols, 32)), 256, 0, st>>>(a, rows, *share);
+    norm_columns_kernel<T, kVec><<<dim3((unsigned)blocks, (unsigned)ceil_div(a.cols, 32 * kVec)), 256, 0, st>>>(a, rows, *share);
     const int64_t most = (int64_t)sms * 4;
-    norm_backward_wide_kernel<T, kWhole ? VEC : 1><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
+    norm_backward_wide_kernel<T, kVec><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
   }
 }
 
