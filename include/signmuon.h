@@ -347,8 +347,9 @@ signmuon_status signmuon_momentum_norm_noalloc(const signmuon_shape* shapes, int
  * ld >= cols (in elements) and any address that is a multiple of the element
  * size; 16-byte aligned rows of a multiple of 16 bytes run fastest.  Only the
  * workspace has to be 256-byte aligned.  Rows of embeddings and layer norms
- * have at most 2^20 columns (else SIGNMUON_ERR_UNSUPPORTED).  rows = 0 is allowed (row pointers may
- * then be NULL).  Sums are taken in fp32 in an order fixed by the shapes and
+ * have at most 2^20 columns (else SIGNMUON_ERR_UNSUPPORTED).  rows = 0 is
+ * allowed (row pointers may then be NULL).  None of these kernels waits on a
+ * flag in memory: no error word is recorded in the workspace.  Sums are taken in fp32 in an order fixed by the shapes and
  * ids, and rounded once, to nearest, to the output's type: results are
  * bit-reproducible.  Outputs must not overlap inputs unless stated.
  * ---------------------------------------------------------------------- */
@@ -418,8 +419,8 @@ signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const 
  *   row_loss[n] = T^2 * sum over present entries of p * (log p - log q[id]),
  * where an entry whose p underflows to zero counts nothing; an id that comes
  * up more than once holds the sum of its entries' p.  A row without present
- * entries is ignored: loss 0, gradient 0, its logits are not looked at.  With n_m the number of worker m's rows that
- * are not ignored,
+ * entries is ignored: loss 0, gradient 0, whatever its logits are.  With n_m
+ * the number of worker m's rows that are not ignored,
  *   loss[m] = sum of worker m's row losses / max(n_m, 1)
  *   dlogits[n, :] = grad_scale * d loss[m] / d logits[n, :]
  *                 = grad_scale * T * (q - p) / n_m

@@ -23,7 +23,8 @@ the arguments.  The functions are not differentiable by autograd: the backward
 functions are called for that.
 Nothing synchronises, so every call can be captured into a CUDA graph, and
 scratch is allocated per call, so calls on different streams (and captured
-graphs) share nothing.  Tensors are fp32 or bf16 on one CUDA device; rows may
+graphs) share nothing.  The gradients that a call returns for the workers are
+views of one allocation; out may not overlap an input unless stated.  Tensors are fp32 or bf16 on one CUDA device; rows may
 have any stride, columns must be adjacent.  Wrong arguments raise TypeError or
 ValueError, failures in the library SignMuonError.
 """
@@ -107,10 +108,11 @@ def distill_loss(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: torch.
     logits.shape[:-1], and loss[m] the mean over worker m's rows, fp32
     [n_workers].
 
-    temperature: in [1e-6, 1e6].  logits: rows of the vocabulary; top_ids (int32 or int64), top_logits:
+    logits: rows of the vocabulary; top_ids (int32 or int64), top_logits:
     contiguous rows of 1 to 1024 entries; an entry with an id outside the
     vocabulary or a logit of -inf is absent, and a row without entries is
-    ignored (loss 0, not counted in the mean)."""
+    ignored (loss 0, not counted in the mean).  temperature: in [1e-6, 1e6],
+    and logits / temperature within fp32's range."""
     return _load().distill(logits, top_ids, top_logits, n_workers, splits, temperature, 1.0, False, None)[:2]
 
 
