@@ -32,6 +32,7 @@ constexpr int kRowThreads = 512;           // of a block that reads its row twic
 constexpr int kHeldThreads = 384, kHeldBatch = 3;
 constexpr int kStreamThreads = 512, kStreamBatch = 4;
 constexpr int kShortWarps = 8, kShortCols = 1024;  // of a block of short rows; columns of one at most
+constexpr int kWarpBatch = 8;              // vectors a lane loads at a time of a row that a warp has
 constexpr int kDepth = 3;                  // groups under way where a row is not held
 constexpr int kMaxCluster = 8;
 constexpr int kSmSmem = 227 * 1024;
@@ -387,6 +388,96 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The elements of a row up to its first whole 16 bytes (head) and from body_end on
+// are taken one at a time.
+template <typename T>
+struct RowSpan {
+  static constexpr int kVec = 16 / sizeof(T);
+  int head, body_end;
+  __device__ RowSpan(const T* p, int n) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) % 16) / (int)sizeof(T);
+    head = off ? min(kVec - off, n) : 0;
+    body_end = head + (n - head) / kVec * kVec;
+  }
+};
+
+// Losses alone, a warp a row at any address, kWarpBatch vectors a lane under way
+// and no barrier.  Bound by memory where rows are many (8192 rows of 50000: fp32 239
+// us, bf16 132; a block a row, as below, took 262 and 153), by latency else (4479
+// of 6130 bf16 19 us for 33, 600 of 2000 8 for 13).
+template <typename T>
+__global__ void __launch_bounds__(kShortWarps * 32)
+warp_losses_kernel(const RowArgs a) {
+  constexpr int kVec = RowSpan<T>::kVec;
+  allow_next_kernel();
+  wait_for_kernel_before();
+  const int lane = threadIdx.x & 31, n = a.vocab;
+  const int64_t row = (int64_t)blockIdx.x * kShortWarps + threadIdx.x / 32;
+  if (row >= a.rows) return;
+  if (!a.counts[row]) {
+    if (lane == 0) a.row_loss[row] = 0.f;
+    return;
+  }
+  const float c = a.inv_t * kLog2e;
+  const Pair cc(c, c);
+  const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
+  const RowSpan<T> span(z, n);
+  // The ends, fewer than 32 elements.
+  const int ends = span.head + n - span.body_end;
+  Soft soft = {-INFINITY, 0.f};
+  if (lane < ends) {
+    const float v = load_elem(z, lane < span.head ? lane : lane - span.head + span.body_end, sizeof(T) == 2);
+    soft_raise(soft, v, c);
+    soft.s += exp2_fast(fmaf(v, c, soft_ref(soft.e)));
+  }
+  __syncwarp();
+  using Raw = decltype(Chunk<T>::r);
+  const Raw* body = reinterpret_cast<const Raw*>(z + span.head);
+  const int vecs = (span.body_end - span.head) / kVec;
+  for (int at = lane; at - lane < vecs; at += 32 * kWarpBatch) {
+    Chunk<T> x[kWarpBatch];
+#pragma unroll
+    for (int i = 0; i < kWarpBatch; ++i) {
+      x[i].clear();
+      if (at + 32 * i < vecs) x[i].r = __ldcs(body + at + 32 * i);
+    }
+    float top = x[0].max();
+#pragma unroll
+    for (int i = 1; i < kWarpBatch; ++i) top = fmaxf(top, x[i].max());
+    soft_raise(soft, top, c);
+    const Pair ref(soft_ref(soft.e), soft_ref(soft.e));
+    Pair sum(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kWarpBatch; ++i) {
+      Pair v[kVec / 2];
+      x[i].get(v);
+#pragma unroll
+      for (int q = 0; q < kVec / 2; ++q) {
+        const Pair e = fma(v[q], cc, ref);
+        sum = sum + Pair(exp2_fast(e.lo()), exp2_fast(e.hi()));
+      }
+    }
+    soft.s += sum.lo() + sum.hi();
+  }
+  __syncwarp();
+  soft = warp_join(soft);
+  const Entry* entries = a.entries + row * a.top;
+  float cross = 0.f;
+  for (int k0 = lane; k0 < a.top; k0 += 128) {
+    Entry entry[4];
+    float logit[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) entry[j] = k0 + 32 * j < a.top ? entries[k0 + 32 * j] : Entry{-1, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) logit[j] = entry[j].id >= 0 ? load_elem(z, entry[j].id, sizeof(T) == 2) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (entry[j].id >= 0) cross = fmaf(entry[j].p, soft_log(soft, logit[j], c), cross);
+  }
+  cross = warp_sum(cross);
+  if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - cross);
+}
+
 // A thread's chunks of a row: q = 0 .. n - 1 at element q * stride of `at`,
 // which may lie before the row (then the first chunk's first elements do).
 struct Mine {
@@ -704,17 +795,6 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
 // whole 16 bytes are taken one at a time.  (2048 rows of 50000 with their gradient,
 // one element past 16 bytes: bf16 224 us, fp32 372; on 16 bytes, held: 104 and 160.)
 template <typename T>
-struct RowSpan {
-  static constexpr int kVec = 16 / sizeof(T);
-  int head, body_end;
-  __device__ RowSpan(const T* p, int n) {
-    const int off = (int)(reinterpret_cast<uintptr_t>(p) % 16) / (int)sizeof(T);
-    head = off ? min(kVec - off, n) : 0;
-    body_end = head + (n - head) / kVec * kVec;
-  }
-};
-
-template <typename T>
 __global__ void __launch_bounds__(kRowThreads)
 rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
   constexpr int kVec = RowSpan<T>::kVec;
@@ -872,6 +952,12 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
     };
     if (a.dz) by_length(std::true_type());
     else by_length(std::false_type());
+    return;  // the caller asks for the error
+  }
+  // Losses by a warp a row where rows are short, or so many that the SMs have
+  // enough under way all the same: a warp alone reads 3 to 4 GB/s.
+  if (!a.dz && (int64_t)a.vocab * (int64_t)sizeof(T) <= 8192 + 8192 * a.rows / (2 * sms)) {
+    launch_after(warp_losses_kernel<T>, dim3((unsigned)ceil_div(a.rows, kShortWarps)), kShortWarps * 32, 0, st, a);
     return;  // the caller asks for the error
   }
   // More blocks than rows where rows are few.
