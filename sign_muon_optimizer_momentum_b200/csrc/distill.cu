@@ -32,6 +32,7 @@ constexpr int kRowThreads = 512;           // of a block that reads its row twic
 constexpr int kHeldThreads = 384, kHeldBatch = 3;
 constexpr int kStreamThreads = 512, kStreamBatch = 4;
 constexpr int kShortWarps = 8, kShortCols = 1024;  // of a block of short rows; columns of one at most
+constexpr int kLossThreads = 512;          // of a block that adds a worker's losses
 constexpr int kWarpBatch = 8;              // vectors a lane loads at a time of a row that a warp has
 constexpr int kDepth = 3;                  // groups under way where a row is not held
 constexpr int kMaxCluster = 8;
@@ -891,22 +892,23 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
 
 // ---------------------------------------------------------------- workers
 // A block a worker, in a fixed order; 2 us, bound by latency.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kLossThreads)
 worker_loss_kernel(const float* __restrict__ row_loss, const uint8_t* __restrict__ counts, float* __restrict__ loss,
                    const __grid_constant__ WorkerRows workers) {
-  __shared__ double s_sum[8];
-  __shared__ int64_t s_n[8];
+  __shared__ double s_sum[kLossThreads / 32];
+  __shared__ int64_t s_n[kLossThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, m = blockIdx.x;
   wait_for_kernel_before();
   double sum = 0.0;
   int64_t n = 0;
-  for (int64_t i = workers.begin[m] + threadIdx.x; i < workers.begin[m + 1]; i += 256) sum += row_loss[i], n += counts[i];
+#pragma unroll 4
+  for (int64_t i = workers.begin[m] + threadIdx.x; i < workers.begin[m + 1]; i += kLossThreads) sum += row_loss[i], n += counts[i];
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o), n += __shfl_xor_sync(0xffffffffu, n, o);
   if (lane == 0) s_sum[warp] = sum, s_n[warp] = n;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 8; ++i) sum += s_sum[i], n += s_n[i];
+    for (int i = 1; i < kLossThreads / 32; ++i) sum += s_sum[i], n += s_n[i];
     loss[m] = (float)(sum / (double)(n > 0 ? n : 1));
   }
 }
@@ -1133,7 +1135,7 @@ signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_
     else launch_rows<__nv_bfloat16>(a, workers, cs);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
   }
-  launch_after(worker_loss_kernel, dim3((unsigned)n_workers), 256, 0, cs, row_loss, a.counts, loss, workers);
+  launch_after(worker_loss_kernel, dim3((unsigned)n_workers), kLossThreads, 0, cs, row_loss, a.counts, loss, workers);
   return cuda_status(cudaGetLastError());
 }
 
