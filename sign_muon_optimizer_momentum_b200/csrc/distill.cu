@@ -973,13 +973,14 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
     slice = ceil_div(chunks, r);
     const int64_t need = (int64_t)round_up((size_t)ceil_div(slice, batch), 32);
     if (a.dz) {
-      // Blocks that an SM has shared memory and rows for (six, of long rows), and
-      // their share of its threads.
+      // Blocks that an SM has shared memory and rows for, and their share of its
+      // threads.  Eight at most (8000 rows of 3000 bf16, with six, eight, twelve: 50,
+      // 46, 42 us; 5397 of 9487: 71, 66, 72; 2048 of 5000: 24, 21, 25).
       smem = slice * 16 + (int64_t)a.top * 4;
       an_sm = kSmSmem / (smem + 2048);
       const int64_t rows = ceil_div(a.rows * r, sms);
       an_sm = an_sm > rows ? rows : an_sm;
-      an_sm = an_sm < 1 ? 1 : an_sm > 6 ? 6 : an_sm;
+      an_sm = an_sm < 1 ? 1 : an_sm > 8 ? 8 : an_sm;
       threads = (int)(2 * most / an_sm / 32 * 32);
     } else {
       // Fewer threads a row, and more rows at a time, unless that leaves more SMs
@@ -1053,7 +1054,13 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
       else if (threads == 256) launch(grad, std::integral_constant<int, 256>());
       else if (threads == 192) launch(grad, std::integral_constant<int, 192>());
       else if (threads == 128) launch(grad, std::integral_constant<int, 128>());
-      else launch(grad, std::integral_constant<int, 0>());
+      else if constexpr (kMost == kHeldThreads) {
+        if (threads == 96) launch(grad, std::integral_constant<int, 96>());
+        else if (threads == 64) launch(grad, std::integral_constant<int, 64>());
+        else launch(grad, std::integral_constant<int, 0>());
+      } else {
+        launch(grad, std::integral_constant<int, 0>());
+      }
     };
     if (a.dz) by_block(std::true_type());
     else by_block(std::false_type());
