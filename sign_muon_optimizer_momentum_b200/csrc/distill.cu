@@ -893,8 +893,7 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
 // ---------------------------------------------------------------- workers
 // A block a worker, in a fixed order; 2 us, bound by latency.
 __global__ void __launch_bounds__(kLossThreads)
-worker_loss_kernel(const float* __restrict__ row_loss, const uint8_t* __restrict__ counts, float* __restrict__ loss,
-                   const __grid_constant__ WorkerRows workers) {
+worker_loss_kernel(const float* row_loss, const uint8_t* counts, float* loss, const __grid_constant__ WorkerRows workers) {
   __shared__ double s_sum[kLossThreads / 32];
   __shared__ int64_t s_n[kLossThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, m = blockIdx.x;

@@ -314,8 +314,7 @@ sort_tiles_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant
 // runs each, searched in L2 from end to end, took 11 us each.)
 __global__ void __launch_bounds__(kMergeThreads)
 merge_kernel(const __grid_constant__ WorkerRows rows, const __grid_constant__ WorkerBlocks blocks, int n_workers, int run,
-             const uint32_t* __restrict__ key, const uint32_t* __restrict__ tok, uint32_t* __restrict__ out_key,
-             uint32_t* __restrict__ out_tok) {
+             const uint32_t* key, const uint32_t* tok, uint32_t* out_key, uint32_t* out_tok) {
   constexpr int kWarps = kMergeThreads / 32, kSearches = 2 * kFan / kWarps, kSide = 8;
   __shared__ uint32_t s_key[kMergeStage];
   // Of each run: the places of the block's first and behind its last key, from

@@ -140,7 +140,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 // A kernel that follows another one of the same call is launched while that
 // one still runs (launch_after), which hides the launch itself: the first
 // allows it when it starts, the second waits, before it reads or writes
-// anything, until the first is done and its writes are seen.
+// anything, until the first is done and its writes are seen.  What the first
+// writes the second reads through plain pointers: const __restrict__ (or
+// __ldg) would allow loads by the read-only path, or before the wait, of data
+// that still changes.
 __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
