@@ -805,6 +805,8 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
   wait_for_kernel_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, n = a.vocab;
   const float c = a.inv_t * kLog2e;
+  int worker = -1;
+  float scale = 0.f;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
     T* dz = a.dz ? static_cast<T*>(a.dz) + row * a.ld_dz : nullptr;
@@ -850,13 +852,15 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
       if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - x);
     }
     if (!dz) continue;
-    // The rows of this worker that count.
-    int m = 0;
-    while (workers.begin[m + 1] <= row) ++m;
-    const int cnt = __reduce_add_sync(0xffffffffu, count_rows(a.counts, workers.begin[m], workers.begin[m + 1], threadIdx.x, kRowThreads));
-    if (lane == 0) atomicAdd(&s_n, cnt);
-    __syncthreads();
-    const float scale = a.grad_scale * a.t / (float)s_n, qs = scale / soft.s, ref = soft_ref(soft.e);
+    if (worker < 0 || workers.begin[worker + 1] <= row) {
+      // The rows of this row's worker that count.
+      while (workers.begin[++worker + 1] <= row) {}
+      const int cnt = __reduce_add_sync(0xffffffffu, count_rows(a.counts, workers.begin[worker], workers.begin[worker + 1], threadIdx.x, kRowThreads));
+      if (lane == 0) atomicAdd(&s_n, cnt);
+      __syncthreads();
+      scale = a.grad_scale * a.t / (float)s_n;
+    }
+    const float qs = scale / soft.s, ref = soft_ref(soft.e);
     // Entries' logits are read before the gradient may overwrite them.
     float fix[kMaxTop / kRowThreads];
     for (int i = 0, k = threadIdx.x; k < a.top; ++i, k += kRowThreads) {
