@@ -155,16 +155,19 @@ teacher_kernel(int64_t rows, int top, const void* __restrict__ ids, int wide, co
 
 // ------------------------------------------------------------------- rows
 struct RowArgs {
+  const void* top_ids;
+  const void* top_logits;
+  int32_t ids_wide, top_bf16;
   const void* z;
   int64_t ld_z;
   void* dz;  // null: the losses alone
   int64_t ld_dz;
-  const Entry* entries;
+  Entry* entries;
   const float* plogp;
   const uint8_t* counts;
   float* row_loss;
   int64_t rows;
-  int32_t vocab, top, n_workers;
+  int32_t vocab, top;
   float t, inv_t, grad_scale;
 };
 
@@ -172,12 +175,19 @@ struct RowArgs {
 // times the largest z so far.  c z - e is one fused multiply-add, rounded once
 // and only to the size of the difference, and changing e multiplies s by a
 // power of two.  An empty sum has e = -inf and s = 0.
+// That holds while an ulp of c z is at most 1/2.  Logits below -kMaxExponent / c
+// count nothing (a part of a row without others keeps that e, and the parts that
+// have others are infinitely larger); a row whose largest is not above that, or
+// is above kMaxExponent / c, is taken again by left_row.
+constexpr float kMaxExponent = 1 << 22;
 struct Soft {
   float e, s;
 };
+// Whether that is the sum (it is not if any of the row is NaN).
+__device__ __forceinline__ bool soft_holds(Soft a) { return fabsf(a.e) < kMaxExponent && a.s > 0.f && a.s < INFINITY; }
 __device__ __forceinline__ float soft_ref(float e) { return e == -INFINITY ? 0.f : -e; }  // added to c z
 __device__ __forceinline__ void soft_raise(Soft& a, float top, float c) {
-  const float e = ceilf(top * c);
+  const float e = fmaxf(ceilf(top * c), -kMaxExponent);
   if (e > a.e) {
     a.s *= a.e == -INFINITY ? 0.f : exp2_fast(a.e - e);
     a.e = e;
@@ -193,9 +203,11 @@ __device__ __forceinline__ Soft warp_join(Soft a) {
     a = soft_join(a, {__shfl_xor_sync(0xffffffffu, a.e, o), __shfl_xor_sync(0xffffffffu, a.s, o)});
   return a;
 }
-// log q of a logit.
-__device__ __forceinline__ float soft_log(Soft a, float z, float c) {
-  return (fmaf(z, c, -a.e) - log2f(a.s)) * 0.6931471805599453f;
+// log q of a logit.  (Of one so low that c z overflows: z / T, beside which the
+// rest of it is below an ulp.)
+__device__ __forceinline__ float soft_log(Soft a, float z, float c, float inv_t) {
+  const float v = fmaf(z, c, -a.e);
+  return v == -INFINITY ? z * inv_t : (v - log2f(a.s)) * 0.6931471805599453f;
 }
 
 // Thread t's share, of `threads`, of the rows [begin, end) that count, 16 bytes at a time
@@ -215,12 +227,133 @@ __device__ __forceinline__ int count_rows(const uint8_t* counts, int64_t begin, 
   return n;
 }
 
+// -------------------------------------------------------------- rows left
+// A row that fp32 does not give is left by the loop over rows, marked by this NaN
+// (not one that arithmetic gives) as its loss, and taken when the loop is done:
+// there it costs the others no registers.
+constexpr uint32_t kLeft = 0x7fc0deadu;
+__device__ __forceinline__ bool is_left(const RowArgs& a, int64_t row) { return __float_as_uint(a.row_loss[row]) == kLeft; }
+
+// Threads that have a row together: a warp, or a block.
+template <bool kWarp>
+struct Team {
+  __device__ __forceinline__ static int rank() { return kWarp ? threadIdx.x & 31 : threadIdx.x; }
+  __device__ __forceinline__ static int size() { return kWarp ? 32 : blockDim.x; }
+  __device__ __forceinline__ static void sync() {
+    if constexpr (kWarp) __syncwarp();
+    else __syncthreads();
+  }
+  // All get f over their values, joined in a fixed order by way of `sh`, a double
+  // for each warp of a block.  (An array that the kernel has already: where the
+  // dynamic shared memory starts behind the static arrays matters, 2048 x 50000
+  // fp32 losses took 75 us from byte 448, 77 from 512 and 85 from 464.)
+  template <typename F>
+  __device__ __forceinline__ static double join(double v, double* sh, F f) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if constexpr (!kWarp) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) sh[threadIdx.x / 32] = v;
+      __syncthreads();
+      v = sh[0];
+      for (int i = 1; i < (int)blockDim.x / 32; ++i) v = f(v, sh[i]);
+    }
+    return v;
+  }
+  __device__ __forceinline__ static double sum(double v, double* sh) {
+    return join(v, sh, [](double x, double y) { return x + y; });
+  }
+  __device__ __forceinline__ static double max(double v, double* sh) {
+    return join(v, sh, [](double x, double y) { return fmax(x, y); });
+  }
+};
+
+// A row from its definition in fp64, differences before products, with the
+// entries as they were given.  The gradient may take the logits' place; `scale` is
+// its factor.  The row's entries in the workspace are used up.
+template <typename T, bool kGrad, bool kWarp>
+__device__ __forceinline__ void left_row(const RowArgs& a, int64_t row, double scale, double* sh) {
+  using G = Team<kWarp>;
+  const int t = G::rank(), n = G::size();
+  const double inv_t = 1.0 / (double)a.t;
+  const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
+  Entry* entries = a.entries + row * a.top;
+  const auto logit = [&](int i) { return (double)load_elem(z, i, sizeof(T) == 2); };
+  const auto entry = [&](int k, double& u) {  // its id, -1 if it is absent
+    const int64_t id = load_id(a.top_ids, row * a.top + k, a.ids_wide);
+    const float v = load_elem(a.top_logits, row * a.top + k, a.top_bf16);
+    u = v;
+    return id >= 0 && id < a.vocab && v != -INFINITY ? (int)id : -1;
+  };
+  double u, u_top = -INFINITY, su = 0.0, z_top = -INFINITY, sz = 0.0;
+  for (int k = t; k < a.top; k += n)
+    if (entry(k, u) >= 0) u_top = fmax(u_top, u);
+  u_top = G::max(u_top, sh);
+  for (int k = t; k < a.top; k += n)
+    if (entry(k, u) >= 0) su += exp((u - u_top) * inv_t);
+  su = G::sum(su, sh);
+  for (int i = t; i < a.vocab; i += n) z_top = fmax(z_top, logit(i));
+  z_top = G::max(z_top, sh);
+  for (int i = t; i < a.vocab; i += n) sz += exp((logit(i) - z_top) * inv_t);
+  sz = G::sum(sz, sh);
+  const double log_su = log(su), log_sz = log(sz);
+  double kl = 0.0, twice = 0.0;
+  for (int k = t; k < a.top; k += n) {
+    const int id = entry(k, u);
+    if (id < 0) continue;
+    const double x = (u - u_top) * inv_t, p = exp(x) / su, y = (logit(id) - z_top) * inv_t;
+    if ((float)p == 0.f) continue;
+    kl += p * ((x - log_su) - (y - log_sz));
+    if (entries[k].id < 0) twice = 1.0;  // another entry holds this one's p
+  }
+  kl = G::sum(kl, sh);
+  if (t == 0) a.row_loss[row] = (float)((double)a.t * a.t * kl);
+  if constexpr (kGrad) {
+    twice = G::max(twice, sh);
+    for (int k = t; k < a.top; k += n) {
+      const int id = entries[k].id;
+      if (id < 0) continue;
+      double q = exp((logit(id) - z_top) * inv_t) / sz;
+      for (int j = twice > 0.0 ? 0 : k; j < (twice > 0.0 ? a.top : k + 1); ++j)
+        if (entry(j, u) == id) q -= exp((u - u_top) * inv_t) / su;
+      entries[k].p = (float)(q * scale);
+    }
+    G::sync();
+    const double qs = scale / sz;
+    T* dz = static_cast<T*>(a.dz) + row * a.ld_dz;
+    for (int i = t; i < a.vocab; i += n) store_elem(dz, i, sizeof(T) == 2, (float)(exp((logit(i) - z_top) * inv_t) * qs));
+    G::sync();
+    for (int k = t; k < a.top; k += n)
+      if (entries[k].id >= 0) store_elem(dz, entries[k].id, sizeof(T) == 2, entries[k].p);
+  }
+}
+
+// The rows first, first + step, ... of a team that were left.
+template <typename T, bool kGrad, bool kWarp>
+__device__ __forceinline__ void left_rows(const RowArgs& a, const WorkerRows& workers, int64_t first, int64_t end, int64_t step,
+                                          double* sh) {
+  using G = Team<kWarp>;
+  int worker = -1;
+  double scale = 0.0;
+  for (int64_t row = first; row < end; row += step) {
+    if (!a.counts[row] || !is_left(a, row)) continue;
+    G::sync();
+    if (kGrad && (worker < 0 || workers.begin[worker + 1] <= row)) {
+      while (workers.begin[++worker + 1] <= row) {}
+      scale = (double)a.grad_scale * a.t /
+              G::sum(count_rows(a.counts, workers.begin[worker], workers.begin[worker + 1], G::rank(), G::size()), sh);
+    }
+    left_row<T, kGrad, kWarp>(a, row, scale, sh);
+  }
+}
+
 // ------------------------------------------------------------- short rows
 // A warp a row, kE elements a lane in registers: one exponential an element, and
 // no barrier a row.  (5927 rows of 586 bf16 with their gradient: 20 us, where a block
 // a row, as below, took 33; 20000 rows of 193 fp32: 28 for 67 us.)
+// (Blocks an SM: as many as the registers of the loop over rows allow.)
 template <typename T, bool kGrad, int kE>
-__global__ void __launch_bounds__(kShortWarps * 32)
+__global__ void __launch_bounds__(kShortWarps * 32, kE == 32 ? 2 : kGrad ? (kE == 4 ? 5 : 4) : (kE == 4 ? 8 : kE == 8 ? 6 : 5))
 short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, int per_warp) {
   // The teacher's part of the gradient by column, zero but for a row's entries.
   __shared__ float s_sub[kGrad ? kShortWarps : 1][kGrad ? 32 * kE : 1];
@@ -248,6 +381,7 @@ short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, i
     __syncthreads();
   }
   float scale = 0.f;
+  bool left = false;
   for (int64_t row = first; row < last; ++row) {
     const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
     T* dz = kGrad ? static_cast<T*>(a.dz) + row * a.ld_dz : nullptr;
@@ -279,6 +413,11 @@ short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, i
 #pragma unroll
     for (int i = 0; i < kE; ++i) v[i] = exp2_fast(fmaf(v[i], c, ref)), s += v[i];
     const Soft soft = {e, warp_sum(s)};
+    if (!soft_holds(soft)) {
+      if (lane == 0) a.row_loss[row] = __uint_as_float(kLeft);
+      left = true;
+      continue;
+    }
     // The entries, with their logits before the gradient may take their place.
     const Entry* entries = a.entries + row * a.top;
     float cross = 0.f;
@@ -292,7 +431,7 @@ short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, i
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (entry[j].id >= 0) {
-          cross = fmaf(entry[j].p, soft_log(soft, logit[j], c), cross);
+          cross = fmaf(entry[j].p, soft_log(soft, logit[j], c, a.inv_t), cross);
           if constexpr (kGrad) sub[entry[j].id] = entry[j].p * scale;
         }
     }
@@ -309,6 +448,10 @@ short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, i
       }
       __syncwarp();
     }
+  }
+  if (left) {
+    __syncwarp();
+    left_rows<T, kGrad, true>(a, workers, first, last, 1, nullptr);
   }
 }
 
@@ -462,6 +605,10 @@ warp_losses_kernel(const RowArgs a) {
   }
   __syncwarp();
   soft = warp_join(soft);
+  if (!soft_holds(soft)) {
+    left_row<T, false, true>(a, row, 0.0, nullptr);
+    return;
+  }
   const Entry* entries = a.entries + row * a.top;
   float cross = 0.f;
   for (int k0 = lane; k0 < a.top; k0 += 128) {
@@ -473,7 +620,7 @@ warp_losses_kernel(const RowArgs a) {
     for (int j = 0; j < 4; ++j) logit[j] = entry[j].id >= 0 ? load_elem(z, entry[j].id, sizeof(T) == 2) : 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (entry[j].id >= 0) cross = fmaf(entry[j].p, soft_log(soft, logit[j], c), cross);
+      if (entry[j].id >= 0) cross = fmaf(entry[j].p, soft_log(soft, logit[j], c, a.inv_t), cross);
   }
   cross = warp_sum(cross);
   if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - cross);
@@ -527,7 +674,8 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
   constexpr int kMaxWarps = (kGrad ? kHeldThreads : kStreamThreads) / 32;
   // The block's chunks (for the losses kDepth batches), and the entries' logits.
   extern __shared__ __align__(16) uint8_t held[];
-  __shared__ Soft s_soft[2][kMaxWarps], s_block[2][kMaxCluster];
+  __shared__ __align__(8) Soft s_soft[2][kMaxWarps];
+  __shared__ Soft s_block[2][kMaxCluster];
   __shared__ float s_cross[kMaxWarps];
   __shared__ int s_n;
   allow_next_kernel();
@@ -616,6 +764,7 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
   for (int b = 0; b < (kGrad ? batches : kDepth); ++b) fetch_next(b);
   int worker = -1, turn = 0, slot = 0;
   float scale = 0.f;
+  bool left = false;
   // Each thread's first entry, a row ahead, so that nothing waits for it.
   const Entry none = {-1, 0.f};
   Entry entry_next = row < a.rows && (int)threadIdx.x < a.top ? a.entries[row * a.top + threadIdx.x] : none;
@@ -708,10 +857,12 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
       for (uint32_t i = 1; i < ranks; ++i) soft = soft_join(soft, s_block[turn][i]);
     }
 
+    const bool holds = soft_holds(soft);  // the same in all blocks of a cluster
+    left |= !holds;
     // Loss: sum p log q of the entries, a warp's part each.
-    float cross = entry.id >= 0 ? entry.p * soft_log(soft, logit, c) : 0.f;
+    float cross = entry.id >= 0 ? entry.p * soft_log(soft, logit, c, a.inv_t) : 0.f;
     for (int k = threadIdx.x + threads; k < a.top; k += threads)
-      if (entries[k].id >= 0) cross = fmaf(entries[k].p, soft_log(soft, entry_z[k], c), cross);
+      if (entries[k].id >= 0) cross = fmaf(entries[k].p, soft_log(soft, entry_z[k], c, a.inv_t), cross);
     cross = warp_sum(cross);
     if (lane == 0) s_cross[warp] = cross;
     if constexpr (kGrad) {
@@ -737,6 +888,7 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
           o[2 * q] = g.lo(), o[2 * q + 1] = g.hi();
         }
       };
+      if (!holds) now.n = 0, now.ends = ~0u;  // writes nothing
       for (int b = 0; b < batches; ++b, dz += kBatch * stride) {
         const Chunk<T>* from = mine + b * kBatch * threads;
         if (plain(now, b)) {
@@ -769,7 +921,7 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
       const int shift = shift_of(row);
       auto fix = [&](Entry e, float z) {
         const int at = e.id >= 0 ? (e.id + shift) / kVec - first : -1;
-        if (at >= 0 && at < slice)
+        if (at >= 0 && at < slice && holds)
           store_elem(dz_all, row * a.ld_dz + e.id, sizeof(T) == 2, exp2_fast(fmaf(z, c, soft_ref(soft.e))) * qs - e.p * scale);
       };
       fix(entry, logit);
@@ -780,13 +932,17 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
     if (rank == 0 && threadIdx.x == 0) {
       float x = 0.f;
       for (int w = 0; w < warps; ++w) x += s_cross[w];
-      a.row_loss[row] = a.t * a.t * (plogp - x);
+      a.row_loss[row] = holds ? a.t * a.t * (plogp - x) : __uint_as_float(kLeft);
     }
     row = row_next;
     now = row < a.rows ? mine_of(row) : Mine{0, 0, 0, ~0u};
     turn ^= 1;
   }
   if (ranks > 1) cluster_sync();
+  if (left && rank == 0) {
+    __syncthreads();
+    left_rows<T, kGrad, false>(a, workers, blockIdx.x / ranks, a.rows, step, reinterpret_cast<double*>(s_soft));
+  }
 }
 
 // ------------------------------------------------------- rows of any address
@@ -799,7 +955,7 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads)
 rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
   constexpr int kVec = RowSpan<T>::kVec;
-  __shared__ Soft s_soft[kRowThreads / 32];
+  __shared__ __align__(8) Soft s_soft[kRowThreads / 32];
   __shared__ int s_n;
   allow_next_kernel();
   wait_for_kernel_before();
@@ -807,6 +963,7 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
   const float c = a.inv_t * kLog2e;
   int worker = -1;
   float scale = 0.f;
+  bool left = false;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
     T* dz = a.dz ? static_cast<T*>(a.dz) + row * a.ld_dz : nullptr;
@@ -841,12 +998,17 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
     __syncthreads();
     soft = s_soft[0];
     for (int i = 1; i < kRowThreads / 32; ++i) soft = soft_join(soft, s_soft[i]);
+    if (!soft_holds(soft)) {
+      if (threadIdx.x == 0) a.row_loss[row] = __uint_as_float(kLeft);
+      left = true;
+      continue;
+    }
     const Entry* entries = a.entries + row * a.top;
     if (warp == 0) {
       float x = 0.f;
       for (int k = lane; k < a.top; k += 32) {
         const Entry e = entries[k];
-        if (e.id >= 0) x = fmaf(e.p, soft_log(soft, load_elem(z, e.id, sizeof(T) == 2), c), x);
+        if (e.id >= 0) x = fmaf(e.p, soft_log(soft, load_elem(z, e.id, sizeof(T) == 2), c, a.inv_t), x);
       }
       x = warp_sum(x);
       if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - x);
@@ -891,6 +1053,11 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
       const int id = entries[k].id;
       if (id >= 0) store_elem(dz, id, sizeof(T) == 2, fix[i]);
     }
+  }
+  if (left) {
+    __syncthreads();
+    if (a.dz) left_rows<T, true, false>(a, workers, blockIdx.x, a.rows, gridDim.x, reinterpret_cast<double*>(s_soft));
+    else left_rows<T, false, false>(a, workers, blockIdx.x, a.rows, gridDim.x, reinterpret_cast<double*>(s_soft));
   }
 }
 
@@ -1120,7 +1287,8 @@ signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_
   a.entries = reinterpret_cast<Entry*>(ws + l.entries);
   a.plogp = reinterpret_cast<float*>(ws + l.plogp);
   a.counts = ws + l.counts;
-  a.row_loss = row_loss, a.rows = n, a.vocab = vocab, a.top = top, a.n_workers = n_workers;
+  a.row_loss = row_loss, a.rows = n, a.vocab = vocab, a.top = top;
+  a.top_ids = top_ids, a.ids_wide = ids_int64 != 0, a.top_logits = top_logits, a.top_bf16 = top_dtype == SIGNMUON_BF16;
   a.t = temperature, a.inv_t = 1.f / temperature, a.grad_scale = grad_scale;
   WorkerRows workers = {};
   for (int m = 0; m <= n_workers; ++m) workers.begin[m] = row_begin[m];

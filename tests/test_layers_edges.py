@@ -27,17 +27,19 @@ def device_ms(f, reps=5):
 
 def distill_bounds(z, u, splits, t, top, ref):
     """What the losses by row and worker and the gradient may be off, from
-    check_distill of test_layers."""
+    check_distill of test_layers.  (A spread counts to 200: what lies further
+    below the largest is e^-200 and less, nothing beside it.)"""
     _, R, D, logq, p, on = ref
-    zd = z.double()
-    spread = torch.where(on, (torch.where(on[:, None], zd, 0.0).amax(1)
-                              - torch.where(on[:, None] & z.isfinite(), zd, float("inf")).amin(1)).clamp(min=0) / t, 0.0)
-    uu = u.double() / t
     inf = float("inf")
-    uspread = torch.where(on, torch.where(u.isfinite(), uu, -inf).amax(1) - torch.where(u.isfinite(), uu, inf).amin(1), 0.0)
+
+    def spread_of(x):
+        x = x.double() / t
+        d = torch.where(x.isfinite(), x, -inf).amax(1) - torch.where(x.isfinite(), x, inf).amin(1)
+        return torch.where(on, d, 0.0).clamp(0.0, 200.0)
+    spread, uspread = spread_of(z), spread_of(u)
     e_q = (4 * spread + 8 + z.shape[1] / 256 + 64) * U
     e_p = (4 * uspread + 8 + top) * U
-    size = (p * logq.clamp(min=-1e30).abs()).sum(1) + torch.special.entr(p).sum(1).abs()
+    size = (p * logq.clamp(min=-1e38)).abs().sum(1) + torch.special.entr(p).sum(1).abs()
     e_row = t * t * (e_q + e_p + (e_p + 8 * U) * size + top * U * (size + spread) + 8 * U * (spread + 1)) + U * R.abs()
     e_loss, e_dz = [], torch.zeros_like(D)
     for a, b in zip(splits, splits[1:]):
@@ -82,3 +84,55 @@ def test_distill_misaligned_gradient_grows_with_its_rows(cuda_lib):
         out = torch.empty(n, 1101, dtype=BF16, device="cuda")[:, 1:]
         return device_ms(lambda: layers.distill_loss_and_grad(z, ids, u, out=out))
     assert ms(200000) <= 14 * ms(20000)
+
+
+def check_distill_calls(z, ids, u, splits, t, top):
+    """Losses alone, with the gradient, and with it in the logits' place."""
+    n = len(splits) - 1
+    t32 = torch.tensor(t).item()                 # the temperature as fp32 has it
+    ref = distill_reference(z, ids, u, splits, t32)
+    bounds = distill_bounds(z, u, splits, t32, top, ref)
+    check_result(layers.distill_loss(z, ids, u, n, splits, temperature=t), ref, bounds)
+    got = layers.distill_loss_and_grad(z, ids, u, n, splits, temperature=t)
+    check_result(got, ref, bounds)
+    again = layers.distill_loss_and_grad(z, ids, u, n, splits, temperature=t)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    check_result(layers.distill_loss_and_grad(z, ids, u, n, splits, temperature=t, out=z), ref, bounds)
+
+
+LARGE = [  # vocab, rows of one kind, columns before the logits in their buffer (off 16 bytes: another kernel)
+    (40, 3, 0), (300, 3, 0), (900, 40, 0), (3000, 2, 0), (3000, 60, 0), (20001, 2, 0), (131101, 1, 0), (1100, 2, 1), (70001, 1, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab,each,offset", LARGE)
+@pytest.mark.parametrize("kind", ["plain", "twice"])
+def test_distill_rows_of_large_logits(cuda_lib, dtype, vocab, each, offset, kind):
+    """Rows at a mask's value from end to end, from the middle on, and with one
+    logit far above the others, among ordinary rows."""
+    lowest = torch.finfo(dtype).min
+    whole = [1e10, -1e10, -1e30, lowest, 3e9, 5e6, 2.5e6, -5e6, -2.5e6]
+    part = [-1e9, -1e10, -1e30, lowest, -5e6]
+    kinds = len(whole) + len(part) + 4
+    z, ids, u, splits = distill_inputs([each * kinds // 2, each * kinds - each * kinds // 2], vocab, 8, dtype, kind)
+    for i in range(each):
+        rows = z[i * kinds:(i + 1) * kinds]
+        for j, v in enumerate(whole):
+            rows[j] = v
+        for j, v in enumerate(part):
+            rows[len(whole) + j, vocab // 2:] = v
+        rows[-1, vocab // 3] = 1e10
+        rows[-2, vocab // 3] = 5e6
+        rows[-3] += 3e6             # spread by the type's steps
+        ids[i * kinds + 2 * i % kinds] = -1
+    check_distill_calls(padded(z, 3, offset=1) if offset else z, ids, u, splits, 1.0, 8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab", [200, 5000])
+@pytest.mark.parametrize("temperature,std", [(1e-6, 2.0), (1e-6, 1e-7), (1e-3, 3000.0), (1e6, 1e7)])
+def test_distill_temperatures_at_the_ends(cuda_lib, dtype, vocab, temperature, std):
+    z, ids, u, splits = distill_inputs([30, 7], vocab, 9, dtype, "plain")
+    check_distill_calls((z.float() * (std / 2)).to(dtype), ids, u * std, splits, temperature, 9)
