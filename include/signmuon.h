@@ -430,7 +430,11 @@ signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const 
  * [n_workers]; dlogits: device [rows, ld_d] of dtype, NULL for the losses
  * alone (it may be logits itself, with the same stride).
  * 1e-6 <= temperature <= 1e6; logits / temperature have to stay in fp32's
- * range.  At most 2^30 rows, and 2^30 columns (else SIGNMUON_ERR_UNSUPPORTED).
+ * range (masks of -1e30 or the type's lowest value are fine, whole rows of them
+ * too).  The sums are fp32, which gives a row's divergence to about 1e-6 (times
+ * 1 + its entropies), and T^2 times that the loss; above T = 8 rows of a
+ * divergence below 1/16, and at any T rows whose largest logit is above about
+ * 2.9e6 T or below -2.9e6 T, are computed in fp64 and rounded once.  At most 2^30 rows, and 2^30 columns (else SIGNMUON_ERR_UNSUPPORTED).
  * workspace: device, >= signmuon_distill_workspace_bytes(...). */
 size_t signmuon_distill_workspace_bytes(int64_t rows, int top);
 signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_t* row_begin,

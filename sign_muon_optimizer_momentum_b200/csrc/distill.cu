@@ -38,6 +38,12 @@ constexpr int kDepth = 3;                  // groups under way where a row is no
 constexpr int kMaxCluster = 8;
 constexpr int kSmSmem = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
+// The divergence of a row is a difference of sums that fp32 gives to about 1e-6,
+// and T^2 multiplies that.  Above kFineT rows of a divergence below kFineKl (a
+// teacher that covers most of the vocabulary: T^2 times the divergence stays, the
+// sums grow nearly equal) are taken again by left_row, so that a row's loss is off
+// by 6e-5 at most, or by 2e-5 of itself.
+constexpr float kFineT = 8.f, kFineKl = 1.f / 16;
 
 // A teacher's entry: its id (-1: none) and the probability it holds.
 struct Entry {
@@ -169,6 +175,7 @@ struct RowArgs {
   int64_t rows;
   int32_t vocab, top;
   float t, inv_t, grad_scale;
+  float min_kl;  // divergence from which on fp32 does (-inf: always)
 };
 
 // A sum of 2^(c z) as s 2^e, c = log2(e) / T and e a whole number, at least c
@@ -203,11 +210,9 @@ __device__ __forceinline__ Soft warp_join(Soft a) {
     a = soft_join(a, {__shfl_xor_sync(0xffffffffu, a.e, o), __shfl_xor_sync(0xffffffffu, a.s, o)});
   return a;
 }
-// log q of a logit.  (Of one so low that c z overflows: z / T, beside which the
-// rest of it is below an ulp.)
-__device__ __forceinline__ float soft_log(Soft a, float z, float c, float inv_t) {
-  const float v = fmaf(z, c, -a.e);
-  return v == -INFINITY ? z * inv_t : (v - log2f(a.s)) * 0.6931471805599453f;
+// log q of a logit, by way of half its size: c z may overflow where z / T does not.
+__device__ __forceinline__ float soft_log(Soft a, float z, float c) {
+  return (fmaf(z, 0.5f * c, -0.5f * a.e) - 0.5f * log2f(a.s)) * 1.3862943611198906f;
 }
 
 // Thread t's share, of `threads`, of the rows [begin, end) that count, 16 bytes at a time
@@ -352,7 +357,7 @@ __device__ __forceinline__ void left_rows(const RowArgs& a, const WorkerRows& wo
 // no barrier a row.  (5927 rows of 586 bf16 with their gradient: 20 us, where a block
 // a row, as below, took 33; 20000 rows of 193 fp32: 28 for 67 us.)
 // (Blocks an SM: as many as the registers of the loop over rows allow.)
-template <typename T, bool kGrad, int kE>
+template <typename T, bool kGrad, int kE, bool kFine>
 __global__ void __launch_bounds__(kShortWarps * 32, kE == 32 ? 2 : kGrad ? (kE == 4 ? 5 : 4) : (kE == 4 ? 8 : kE == 8 ? 6 : 5))
 short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, int per_warp) {
   // The teacher's part of the gradient by column, zero but for a row's entries.
@@ -431,12 +436,23 @@ short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, i
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (entry[j].id >= 0) {
-          cross = fmaf(entry[j].p, soft_log(soft, logit[j], c, a.inv_t), cross);
+          cross = fmaf(entry[j].p, soft_log(soft, logit[j], c), cross);
           if constexpr (kGrad) sub[entry[j].id] = entry[j].p * scale;
         }
     }
     cross = warp_sum(cross);
-    if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - cross);
+    const float kl = lane == 0 || kFine ? a.plogp[row] - cross : 0.f;
+    if (kFine && !(kl >= a.min_kl)) {
+      if (lane == 0) a.row_loss[row] = __uint_as_float(kLeft);
+      left = true;
+      if constexpr (kGrad) {
+        __syncwarp();
+        for (int i = lane; i < n; i += 32) sub[i] = 0.f;
+        __syncwarp();
+      }
+      continue;
+    }
+    if (lane == 0) a.row_loss[row] = a.t * a.t * kl;
     if constexpr (kGrad) {
       const float qs = scale / soft.s;
       __syncwarp();
@@ -620,10 +636,15 @@ warp_losses_kernel(const RowArgs a) {
     for (int j = 0; j < 4; ++j) logit[j] = entry[j].id >= 0 ? load_elem(z, entry[j].id, sizeof(T) == 2) : 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (entry[j].id >= 0) cross = fmaf(entry[j].p, soft_log(soft, logit[j], c, a.inv_t), cross);
+      if (entry[j].id >= 0) cross = fmaf(entry[j].p, soft_log(soft, logit[j], c), cross);
   }
   cross = warp_sum(cross);
-  if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - cross);
+  const float kl = a.plogp[row] - cross;
+  if (a.min_kl > 0.f && !(kl >= a.min_kl)) {
+    left_row<T, false, true>(a, row, 0.0, nullptr);
+    return;
+  }
+  if (lane == 0) a.row_loss[row] = a.t * a.t * kl;
 }
 
 // A thread's chunks of a row: q = 0 .. n - 1 at element q * stride of `at`,
@@ -857,14 +878,20 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
       for (uint32_t i = 1; i < ranks; ++i) soft = soft_join(soft, s_block[turn][i]);
     }
 
-    const bool holds = soft_holds(soft);  // the same in all blocks of a cluster
-    left |= !holds;
+    bool holds = soft_holds(soft);  // the same in all blocks of a cluster
     // Loss: sum p log q of the entries, a warp's part each.
-    float cross = entry.id >= 0 ? entry.p * soft_log(soft, logit, c, a.inv_t) : 0.f;
+    float cross = entry.id >= 0 ? entry.p * soft_log(soft, logit, c) : 0.f;
     for (int k = threadIdx.x + threads; k < a.top; k += threads)
-      if (entries[k].id >= 0) cross = fmaf(entries[k].p, soft_log(soft, entry_z[k], c, a.inv_t), cross);
+      if (entries[k].id >= 0) cross = fmaf(entries[k].p, soft_log(soft, entry_z[k], c), cross);
     cross = warp_sum(cross);
     if (lane == 0) s_cross[warp] = cross;
+    if (a.min_kl > 0.f) {
+      __syncthreads();
+      float kl = a.plogp[row];
+      for (int w = 0; w < warps; ++w) kl -= s_cross[w];
+      holds &= kl >= a.min_kl;
+    }
+    left |= !holds;
     if constexpr (kGrad) {
       if (worker < 0 || workers.begin[worker + 1] <= row) {
         // The rows that count of this row's worker.
@@ -957,6 +984,7 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
   constexpr int kVec = RowSpan<T>::kVec;
   __shared__ __align__(8) Soft s_soft[kRowThreads / 32];
   __shared__ int s_n;
+  __shared__ bool s_off;
   allow_next_kernel();
   wait_for_kernel_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, n = a.vocab;
@@ -1008,10 +1036,18 @@ rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
       float x = 0.f;
       for (int k = lane; k < a.top; k += 32) {
         const Entry e = entries[k];
-        if (e.id >= 0) x = fmaf(e.p, soft_log(soft, load_elem(z, e.id, sizeof(T) == 2), c, a.inv_t), x);
+        if (e.id >= 0) x = fmaf(e.p, soft_log(soft, load_elem(z, e.id, sizeof(T) == 2), c), x);
       }
-      x = warp_sum(x);
-      if (lane == 0) a.row_loss[row] = a.t * a.t * (a.plogp[row] - x);
+      const float kl = a.plogp[row] - warp_sum(x);
+      const bool off = a.min_kl > 0.f && !(kl >= a.min_kl);
+      if (lane == 0) a.row_loss[row] = off ? __uint_as_float(kLeft) : a.t * a.t * kl, s_off = off;
+    }
+    if (a.min_kl > 0.f) {
+      __syncthreads();
+      if (s_off) {
+        left = true;
+        continue;
+      }
     }
     if (!dz) continue;
     if (worker < 0 || workers.begin[worker + 1] <= row) {
@@ -1109,12 +1145,17 @@ void launch_rows(const RowArgs& a, const WorkerRows& workers, cudaStream_t st) {
   constexpr int kVec = Chunk<T>::kVec;
   const int sms = current_sms();
   if (a.vocab <= kShortCols) {
-    auto launch = [&](auto grad, auto per_lane) {
-      constexpr auto k = short_rows_kernel<T, decltype(grad)::value, decltype(per_lane)::value>;
+    auto launch_one = [&](auto grad, auto per_lane, auto fine) {
+      constexpr auto k = short_rows_kernel<T, decltype(grad)::value, decltype(per_lane)::value, decltype(fine)::value>;
       const int64_t most = (int64_t)sms * resident_blocks<k>(kShortWarps * 32, 0) * kShortWarps;
       const int per_warp = (int)ceil_div(a.rows, most);
       launch_after(k, dim3((unsigned)ceil_div(a.rows, (int64_t)per_warp * kShortWarps)), kShortWarps * 32, 0, st, a, workers,
                    per_warp);
+    };
+    auto launch = [&](auto grad, auto per_lane) {
+      // (The test of a row's divergence costs the gradient's kernels up to 4 %.)
+      if (!decltype(grad)::value || a.min_kl > 0.f) launch_one(grad, per_lane, std::true_type());
+      else launch_one(grad, per_lane, std::bool_constant<!decltype(grad)::value>());
     };
     auto by_length = [&](auto grad) {
       if (a.vocab <= 128) launch(grad, std::integral_constant<int, 4>());
@@ -1290,6 +1331,7 @@ signmuon_status signmuon_distill_loss(int32_t vocab, int n_workers, const int64_
   a.row_loss = row_loss, a.rows = n, a.vocab = vocab, a.top = top;
   a.top_ids = top_ids, a.ids_wide = ids_int64 != 0, a.top_logits = top_logits, a.top_bf16 = top_dtype == SIGNMUON_BF16;
   a.t = temperature, a.inv_t = 1.f / temperature, a.grad_scale = grad_scale;
+  a.min_kl = temperature > kFineT ? kFineKl : -INFINITY;
   WorkerRows workers = {};
   for (int m = 0; m <= n_workers; ++m) workers.begin[m] = row_begin[m];
   if (n) {

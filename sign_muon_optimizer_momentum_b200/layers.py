@@ -112,7 +112,10 @@ def distill_loss(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: torch.
     contiguous rows of 1 to 1024 entries; an entry with an id outside the
     vocabulary or a logit of -inf is absent, and a row without entries is
     ignored (loss 0, not counted in the mean).  temperature: in [1e-6, 1e6],
-    and logits / temperature within fp32's range."""
+    and logits / temperature within fp32's range.  Sums are fp32; rows that it
+    does not give (logits of millions of temperatures, small divergences at
+    temperatures above 8) are computed in fp64, which takes several times as
+    long."""
     return _load().distill(logits, top_ids, top_logits, n_workers, splits, temperature, 1.0, False, None)[:2]
 
 

@@ -136,3 +136,60 @@ def test_distill_rows_of_large_logits(cuda_lib, dtype, vocab, each, offset, kind
 def test_distill_temperatures_at_the_ends(cuda_lib, dtype, vocab, temperature, std):
     z, ids, u, splits = distill_inputs([30, 7], vocab, 9, dtype, "plain")
     check_distill_calls((z.float() * (std / 2)).to(dtype), ids, u * std, splits, temperature, 9)
+
+
+FINE = [  # rows by worker, vocab, columns that are not -inf, entries, columns before the logits in their buffer
+    ([5, 6], 64, 64, 64, 0), ([40, 3], 512, 512, 512, 0), ([9], 1024, 1024, 1024, 0), ([7], 300, 300, 20, 0),
+    ([6, 5], 1500, 600, 600, 0), ([300], 1100, 1000, 1000, 0), ([7], 5000, 700, 700, 0), ([2], 131101, 900, 900, 0),
+    ([5, 4], 1500, 600, 600, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shares,vocab,finite,top,offset", FINE)
+@pytest.mark.parametrize("temperature", [9.0, 30.0, 100.0, 1000.0, 1e5])
+def test_distill_high_temperatures(cuda_lib, dtype, shares, vocab, finite, top, offset, temperature):
+    """Teachers that cover all of the vocabulary that there is, whose divergence
+    falls as 1 / T^2, and one that does not.
+
+    In units of T^2: sums of at most 64 terms one after another of exponentials
+    off by 4 U, twice, and the teacher's entropy (at most log 1024 < 7 times
+    what its p are off), 128 + 7 * 80 < 700 U < 2^-14 in all, of at least 1/16
+    where fp32 is used: 2^-10 of it.  Else fp64: values of at most 16 after a
+    few hundred roundings of 2^-53, at most 2^-40 for kernel and reference, and a
+    rounding to fp32."""
+    n, t = sum(shares), temperature
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n * vocab + top)
+    z = torch.randn(n, vocab, generator=g, device="cuda") * 2
+    z[:, finite:] = -float("inf")
+    z = z.to(dtype)
+    ids = torch.rand(n, finite, generator=g, device="cuda").topk(top, dim=1).indices
+    u = torch.randn(n, top, generator=g, device="cuda") * 1.5
+    if top > 64:
+        # One id twice in some rows, an entry short in others.
+        ids[::3, 5] = ids[::3, 60]
+        ids[1::3, 7] = -1
+    ids[n // 2] = -1
+    splits = [sum(shares[:i]) for i in range(len(shares) + 1)]
+    ref = distill_reference(z, ids, u, splits, t)
+    _, R, D, logq, p, on = ref
+    e_row = R.abs() * 2.0 ** -10 + t * t * 2.0 ** -40
+    low = R / (t * t) < 2.0 ** -4 * (1 - 2.0 ** -9)          # those that fp64 has
+    tight = R.abs() * 2 * U + t * t * 2.0 ** -40
+    e_row = torch.where(low, tight, e_row)
+    _, _, e_dz = distill_bounds(z, u, splits, t, top, ref)
+    e_loss = []
+    for a, b in zip(splits, splits[1:]):
+        k = max(int(on[a:b].sum()), 1)
+        e_loss.append((e_row[a:b] + U * R[a:b].abs()).sum() / k)
+        exact = (half(dtype) + 2 * U) * D[a:b].abs() + t / k * 2.0 ** -40 * (logq[a:b].exp() + p[a:b]) + 2.0 ** -126
+        e_dz[a:b] = torch.where(low[a:b, None], exact, e_dz[a:b])
+    bounds = torch.stack(e_loss), e_row, e_dz
+    if offset:
+        z = padded(z, 3, offset=offset)
+    m = len(shares)
+    check_result(layers.distill_loss(z, ids, u, m, splits, temperature=t), ref, bounds)
+    got = layers.distill_loss_and_grad(z, ids, u, m, splits, temperature=t)
+    check_result(got, ref, bounds)
+    check_result(layers.distill_loss_and_grad(z, ids, u, m, splits, temperature=t, out=z), ref, bounds)
