@@ -115,7 +115,10 @@ def distill_loss(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: torch.
     and logits / temperature within fp32's range.  Sums are fp32; rows that it
     does not give (logits of millions of temperatures, small divergences at
     temperatures above 8) are computed in fp64, which takes several times as
-    long."""
+    long.
+
+    One entry a row at temperature 1 is the cross entropy against next tokens:
+    top_ids = targets[:, None], top_logits = zeros."""
     return _load().distill(logits, top_ids, top_logits, n_workers, splits, temperature, 1.0, False, None)[:2]
 
 

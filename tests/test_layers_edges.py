@@ -193,3 +193,25 @@ def test_distill_high_temperatures(cuda_lib, dtype, shares, vocab, finite, top, 
     got = layers.distill_loss_and_grad(z, ids, u, m, splits, temperature=t)
     check_result(got, ref, bounds)
     check_result(layers.distill_loss_and_grad(z, ids, u, m, splits, temperature=t, out=z), ref, bounds)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_distill_against_next_tokens_is_cross_entropy(cuda_lib, dtype):
+    """One entry a row at temperature 1; negative targets are ignored."""
+    n, vocab = 37, 2001
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    z = (torch.randn(n, vocab, generator=g, device="cuda") * 2).to(dtype)
+    target = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    target[::5] = -100
+    Z = z.double().requires_grad_()
+    ref = torch.nn.functional.cross_entropy(Z, target, ignore_index=-100)
+    ref.backward()
+    loss, row, dz = layers.distill_loss_and_grad(z, target[:, None].contiguous(), torch.zeros(n, 1, device="cuda"))
+    # Sums of at most 64 terms of exponentials off by 4 U and arguments of at most 20 (8 U each).
+    bound = (64 + 4 + 8 * 20) * U
+    assert abs(loss[0].double() - ref.detach()) <= bound
+    q = torch.softmax(Z.detach(), 1) / int((target >= 0).sum())
+    assert ((dz.double() - Z.grad).abs() <= bound * q + (half(dtype) + 4 * U) * Z.grad.abs() * (1 + bound)).all()
+    assert not dz[::5].any() and not row[::5].any()
