@@ -3,15 +3,18 @@ Python binding of layers.py (_layers_native.so, host code only).
 
 Usage: ``python -m sign_muon_optimizer_momentum_b200.build`` (or through
 ``__graft_entry__.build()``).  Both are rebuilt only when a source or header is
-newer than one of them.
+newer than one of them.  The library needs nvcc alone: where PyTorch or
+Python's headers are not installed it is built without the binding.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -36,8 +39,6 @@ def _nvcc() -> str:
 
 def _compile_binding(verbose: bool) -> str:
     """Object file of the PyTorch binding (g++; PyTorch's headers and flags)."""
-    import sysconfig
-
     import torch
     from torch.utils import cpp_extension
     obj = os.path.join(BUILD, "layers_binding.o")
@@ -51,6 +52,11 @@ def _compile_binding(verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError("g++ failed on layers_binding.cpp")
     return obj
+
+
+def _binding_can_be_built() -> bool:
+    headers = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    return importlib.util.find_spec("torch") is not None and os.path.exists(headers)
 
 
 def _link_binding(obj: str) -> None:
@@ -74,7 +80,9 @@ def _newest_input() -> float:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _newest_input() for f in (LIB, BINDING)):
+    with_binding = _binding_can_be_built()
+    made = (LIB, BINDING) if with_binding else (LIB,)
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _newest_input() for f in made):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -91,9 +99,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding, verbose)
+        binding = ex.submit(_compile_binding, verbose) if with_binding else None
         objs = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -101,7 +108,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         raise RuntimeError("link of libsignmuon.so failed")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    if binding is None:
+        sys.stderr.write("PyTorch or Python's headers are missing: built libsignmuon.so without the binding of layers.py\n")
+    else:
+        _link_binding(binding.result())
     return LIB
 
 

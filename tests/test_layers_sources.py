@@ -1,10 +1,15 @@
 """What the token operators' sources have to hold that no run would show."""
 import os
 import re
+import shutil
+import subprocess
+import sys
 
 import pytest
 
-CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sign_muon_optimizer_momentum_b200", "csrc")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PACKAGE = os.path.join(ROOT, "sign_muon_optimizer_momentum_b200")
+CSRC = os.path.join(PACKAGE, "csrc")
 
 
 def kernels(name):
@@ -40,3 +45,38 @@ def test_kernels_that_wait_read_by_ordinary_loads(source):
     for name, params, body in found:
         assert "__restrict__" not in params, name
         assert "__ldg" not in body, name
+
+
+def run_build(tmp_path, *flags, code="print(build.build())"):
+    """build() of a copy of the package, with a stand-in for nvcc, by a Python
+    that is started with `flags`."""
+    package = tmp_path / "sign_muon_optimizer_momentum_b200"
+    shutil.copytree(CSRC, package / "csrc")
+    shutil.copytree(os.path.join(ROOT, "include"), tmp_path / "include")
+    shutil.copy(os.path.join(PACKAGE, "build.py"), package)
+    (package / "__init__.py").write_text("")
+    tools = tmp_path / "tools"
+    tools.mkdir()
+    (tools / "nvcc").write_text('#!/bin/sh\nwhile [ $# -gt 0 ]; do [ "$1" = -o ] && : > "$2"; shift; done\n')
+    (tools / "nvcc").chmod(0o755)
+    env = dict(os.environ, PATH=f"{tools}:{os.environ['PATH']}")
+    env.pop("PYTHONPATH", None)
+    r = subprocess.run([sys.executable, *flags, "-c", f"import sys; sys.path.insert(0, {str(tmp_path)!r})\n"
+                        f"from sign_muon_optimizer_momentum_b200 import build\n{code}"],
+                       capture_output=True, text=True, env=env, timeout=300)
+    return r, package
+
+
+def test_library_is_built_without_pytorch(tmp_path):
+    r, package = run_build(tmp_path, "-S")       # no site-packages: no PyTorch
+    assert r.returncode == 0, r.stderr
+    assert (package / "libsignmuon.so").exists() and not (package / "_layers_native.so").exists()
+    assert "without the binding" in r.stderr
+
+
+def test_library_is_built_where_the_binding_fails(tmp_path):
+    fail = ("def fail(verbose):\n    raise RuntimeError('no binding')\n"
+            "build._binding_can_be_built = lambda: True\nbuild._compile_binding = fail\nbuild.build()")
+    r, package = run_build(tmp_path, "-S", code=fail)
+    assert r.returncode != 0 and "no binding" in r.stderr
+    assert (package / "libsignmuon.so").exists()
