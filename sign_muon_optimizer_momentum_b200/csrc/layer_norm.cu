@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kThreads = 256;         // threads a block for rows of up to that many
 constexpr int kWideThreads = 512;     // threads a block for rows that registers do not hold
+constexpr int kBwdHeldCols = 8192;    // the backward's widest rows that they hold
 
 // Rows and columns of one call.
 struct NormArgs {
@@ -648,7 +649,7 @@ bool by_span(int span, F f) {
   if constexpr (kBackward) {
     if (span <= 2048) return f(Int<16>(), Int<128>());
     if (span <= 4096) return f(Int<16>(), Int<256>());
-    if (span <= 8192) return f(Int<16>(), Int<512>());
+    if (span <= kBwdHeldCols) return f(Int<16>(), Int<512>());
   } else {
     if (span <= 1536) return f(Int<24>(), Int<64>());
     if (span <= 2048) return f(Int<32>(), Int<64>());
@@ -696,9 +697,21 @@ int block_share(int n_workers, const int64_t* row_begin, int rows_a_block, int m
 }
 
 constexpr int kBwdBlocksPerSm = 8;
-// Of blocks at most: those of every SM, and a period (at most 8) more for each
-// worker whose share rounds to none.
-int bwd_max_blocks(int sms, int n_workers) { return sms * kBwdBlocksPerSm + 8 * n_workers; }
+constexpr int kColumnRows = 64;     // rows a block of their column sums at least
+constexpr int kMaxPeriod = 8;
+// Blocks at most, whatever the type and the addresses: those of every SM (the
+// column sums have one) and for each worker whose share rounds to none a period
+// more, and no more than a worker has rows for.
+int64_t bwd_max_blocks(int sms, int32_t cols, int n_workers, const int64_t* row_begin) {
+  const bool wide = cols > kBwdHeldCols;
+  const int64_t most = wide ? (int64_t)sms + n_workers : (int64_t)sms * kBwdBlocksPerSm + kMaxPeriod * n_workers;
+  int64_t useful = 0;
+  for (int m = 0; m < n_workers; ++m) {
+    const int64_t rows = row_begin[m + 1] - row_begin[m];
+    if (rows) useful += wide ? ceil_div(rows, kColumnRows) : rows + kMaxPeriod - 1;
+  }
+  return useful < most ? useful : most;
+}
 
 template <typename T, int VEC, bool kWhole>
 void backward_launch(const NormArgs& a, const WorkerRows& rows, const int64_t* row_begin, int sms, WorkerBlocks* share,
@@ -717,7 +730,7 @@ void backward_launch(const NormArgs& a, const WorkerRows& rows, const int64_t* r
   if (!held) {
     // The column sums first: dx may take dy's place.
     constexpr int kVec = kWhole ? VEC : 1;
-    const int blocks = block_share(a.n_workers, row_begin, 64, sms, 1, share);
+    const int blocks = block_share(a.n_workers, row_begin, kColumnRows, sms, 1, share);
     norm_columns_kernel<T, kVec><<<dim3((unsigned)blocks, (unsigned)ceil_div(a.cols, 32 * kVec)), 256, 0, st>>>(a, rows, *share);
     const int64_t most = (int64_t)sms * 4;
     norm_backward_wide_kernel<T, kVec><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, st>>>(a);
@@ -789,7 +802,7 @@ size_t signmuon_layer_norm_backward_workspace_bytes(int32_t cols, int n_workers,
   if (cols <= 0 || n_workers <= 0 || n_workers > SIGNMUON_MAX_WORKERS || !row_begin ||
       !valid_splits(row_begin, n_workers, row_begin[n_workers]))
     return 0;
-  return kWsHeaderBytes + round_up((size_t)bwd_max_blocks(current_sms(), n_workers) * 2 * cols * 4, 256);
+  return kWsHeaderBytes + round_up((size_t)bwd_max_blocks(current_sms(), cols, n_workers, row_begin) * 2 * cols * 4, 256);
 }
 
 signmuon_status signmuon_layer_norm_backward(int32_t cols, int n_workers, const int64_t* row_begin,

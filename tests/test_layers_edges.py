@@ -6,8 +6,9 @@ Bounds as in test_layers: U = 2^-24 is the most an fp32 rounding is off,
 import pytest
 import torch
 
+from sign_muon_optimizer_momentum_b200 import _lib as L
 from sign_muon_optimizer_momentum_b200 import layers
-from test_layers import BF16, F32, U, distill_inputs, distill_reference, half, padded
+from test_layers import BF16, F32, U, distill_inputs, distill_reference, half, lib, padded  # noqa: F401
 
 
 def device_ms(f, reps=5):
@@ -215,3 +216,71 @@ def test_distill_against_next_tokens_is_cross_entropy(cuda_lib, dtype):
     q = torch.softmax(Z.detach(), 1) / int((target >= 0).sum())
     assert ((dz.double() - Z.grad).abs() <= bound * q + (half(dtype) + 4 * U) * Z.grad.abs() * (1 + bound)).all()
     assert not dz[::5].any() and not row[::5].any()
+
+
+def test_layer_norm_workspace_is_of_the_size_of_the_call(lib):
+    """No more partial rows than the call has rows for, or one for each SM and
+    worker where a row is wider than registers hold (148 SMs without a GPU)."""
+    size = L.signmuon_layer_norm_backward_workspace_bytes
+    for cols in (1, 768, 8192, 16384, 1 << 20):
+        row = 2 * 4 * cols
+        assert size(cols, [0, 1]) <= 8 * row + 512 + 256
+        assert size(cols, [0, 3, 3, 5]) <= (5 + 2 * 7) * row + 512
+        assert size(cols, [0, 0]) <= 512
+        rows = [0, 1 << 20, 1 << 21]
+        assert size(cols, rows) <= (148 * (8 if cols <= 8192 else 1) + 16) * row + 512
+    assert size(1 << 20, [0, 1]) <= (8 << 20) + 512
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [1, 7, 64, 999, 2304, 8192, 8193, 20000])
+@pytest.mark.parametrize("shares", [[1], [2, 0, 1], [9, 30], [700] * 9, [60000 // 7] * 7])
+def test_workspaces_end_where_they_are_said_to(cuda_lib, dtype, cols, shares):
+    """Through the C ABI, with workspaces of exactly the size asked for: what
+    lies behind them stays."""
+    if sum(shares) * cols > 1 << 26:
+        shares = shares[:2]
+    rows = [sum(shares[:i]) for i in range(len(shares) + 1)]
+    n, m, code = rows[-1], len(shares), 0 if dtype == F32 else 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(cols + n)
+    x, dy = (torch.randn(n, cols, generator=g, device="cuda").to(dtype) for _ in range(2))
+    w, stat = torch.ones(cols, dtype=dtype, device="cuda"), torch.ones(n, device="cuda")
+
+    def workspace(size):
+        buf = torch.full(((size + 3) // 4 * 4 + 8192,), 77, dtype=torch.uint8, device="cuda")
+        return buf, lambda: bool((buf[size:] == 77).all())
+    stream = torch.cuda.current_stream().cuda_stream
+    for ld in (cols, cols + 1):
+        def rows_of(t):
+            return torch.empty(n, ld, dtype=dtype, device="cuda")[:, :cols].copy_(t)
+        xs, dys, dx = rows_of(x), rows_of(dy), rows_of(x)
+        size = L.signmuon_layer_norm_backward_workspace_bytes(cols, rows)
+        ws, kept = workspace(size)
+        dw, db = torch.zeros(m, cols + 8, dtype=dtype, device="cuda"), torch.zeros(m, cols + 8, dtype=dtype, device="cuda")
+        L.signmuon_layer_norm_backward(cols, rows, code, dys.data_ptr(), ld, xs.data_ptr(), ld, code, w.data_ptr(),
+                                       stat.data_ptr(), stat.data_ptr(), dx.data_ptr(), ld,
+                                       [dw[i].data_ptr() for i in range(m)], [db[i].data_ptr() for i in range(m)],
+                                       ws.data_ptr(), size, stream)
+        assert kept()
+        for i in range(m):
+            # Each sum is of at most n terms, and a rounding.
+            part = dy[rows[i]:rows[i + 1]].double()
+            e = (n + 8) * U * part.abs().sum(0)
+            assert ((db[i, :cols].double() - part.sum(0)).abs() <= e + half(dtype) * (part.sum(0).abs() + e)).all()
+    ids = torch.randint(0, 50, (n,), generator=g, device="cuda")
+    size = L.signmuon_embedding_backward_workspace_bytes((50, cols), rows)
+    ws, kept = workspace(size)
+    table = torch.zeros(m, 50 * cols + 8, dtype=dtype, device="cuda")
+    L.signmuon_embedding_backward((50, cols), rows, 1, ids.data_ptr(), code, dy.data_ptr(), cols, 1.0, 0, code,
+                                  [table[i].data_ptr() for i in range(m)], ws.data_ptr(), size, stream)
+    assert kept() and not table[:, 50 * cols:].any()
+    top = min(cols, 3)
+    size = L.signmuon_distill_workspace_bytes(n, top)
+    ws, kept = workspace(size)
+    loss, row, dz = torch.zeros(m, device="cuda"), torch.zeros(n, device="cuda"), torch.empty_like(x)
+    top_ids = torch.randint(0, cols, (n, top), generator=g, device="cuda")
+    L.signmuon_distill_loss(cols, rows, code, x.data_ptr(), cols, top, 1, top_ids.data_ptr(), 0, stat.repeat(top).data_ptr(),
+                            1.0, 1.0, loss.data_ptr(), row.data_ptr(), dz.data_ptr(), cols, ws.data_ptr(), size, stream)
+    assert kept()
