@@ -91,6 +91,12 @@ void check_apart(const Tensor& out, const Tensor& in, const char* what, bool sam
   TORCH_CHECK_VALUE(s != at::MemOverlapStatus::Partial && (same || s != at::MemOverlapStatus::Full), "out overlaps ", what);
 }
 
+// Tells autograd that a caller's tensor has been written to: a backward pass that
+// saved it then fails instead of using the new values.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 bool check_ids(const Tensor& ids, const char* what, const Tensor& like) {
   check_cuda(ids, what, like);
   const bool wide = ids.scalar_type() == at::kLong;
@@ -178,6 +184,7 @@ Tensor embedding_forward(const Tensor& table, const Tensor& ids, double scale, s
   check_status("signmuon_embedding_forward",
                signmuon_embedding_forward(shape_of(t.n, t.cols), table_code, table.data_ptr(), t.ld, ids.numel(), wide,
                                           ids.data_ptr(), (float)scale, code, y.data_ptr(), ld, call.stream));
+  if (out) written(*out);
   return y;
 }
 
@@ -217,6 +224,8 @@ std::vector<Tensor> embedding_backward(const Tensor& ids, const Tensor& grad_out
                signmuon_embedding_backward(shape, (int)n_workers, rows.data(), wide, ids.data_ptr(), dy_code,
                                            grad_out.data_ptr(), dy.ld, (float)scale, accumulate, code, ptrs.data(),
                                            ws.data_ptr(), ws.nbytes(), call.stream));
+  if (out)
+    for (const Tensor& t : *out) written(t);
   return grads;
 }
 
@@ -250,6 +259,7 @@ std::tuple<Tensor, Tensor, Tensor> layer_norm_forward(const Tensor& x, const Ten
                signmuon_layer_norm_forward(r.n, shape.cols, code, x.data_ptr(), r.ld, w_code, weight.data_ptr(),
                                            bias ? bias->data_ptr() : nullptr, (float)eps, y.data_ptr(), ld,
                                            mean.data_ptr<float>(), rstd.data_ptr<float>(), call.stream));
+  if (out) written(*out);
   return {y, mean, rstd};
 }
 
@@ -288,6 +298,7 @@ std::tuple<Tensor, std::vector<Tensor>, std::optional<std::vector<Tensor>>> laye
                                             rstd.data_ptr<float>(), dx.data_ptr(), ld, ptrs.data(),
                                             bias ? ptrs.data() + n_workers : nullptr, ws.data_ptr(), ws.nbytes(),
                                             call.stream));
+  if (out) written(*out);
   if (!bias) return {dx, std::move(dw), std::nullopt};
   std::vector<Tensor> db(dw.begin() + n_workers, dw.end());
   dw.resize(n_workers);
@@ -328,6 +339,7 @@ std::tuple<Tensor, Tensor, MaybeTensor> distill(const Tensor& logits, const Tens
                                      top_ids.data_ptr(), top_code, top_logits.data_ptr(), (float)temperature,
                                      (float)grad_scale, loss.data_ptr<float>(), row_loss.data_ptr<float>(),
                                      dz ? dz->data_ptr() : nullptr, ld, ws.data_ptr(), ws.nbytes(), call.stream));
+  if (with_grad && out) written(*out);
   return {loss, row_loss, dz};
 }
 

@@ -284,3 +284,34 @@ def test_workspaces_end_where_they_are_said_to(cuda_lib, dtype, cols, shares):
     L.signmuon_distill_loss(cols, rows, code, x.data_ptr(), cols, top, 1, top_ids.data_ptr(), 0, stat.repeat(top).data_ptr(),
                             1.0, 1.0, loss.data_ptr(), row.data_ptr(), dz.data_ptr(), cols, ws.data_ptr(), size, stream)
     assert kept()
+
+
+@pytest.mark.gpu
+def test_autograd_sees_what_is_written(cuda_lib):
+    """A tensor that a backward pass has saved and a call then writes to fails
+    that pass; tensors of inference mode, which have no versions, are written
+    to all the same."""
+    x = torch.randn(8, 16, device="cuda")
+    w, stat, ids = torch.ones(16, device="cuda"), torch.ones(8, device="cuda"), torch.arange(8, device="cuda")
+    calls = [
+        lambda out: layers.embedding_forward(x, ids, out=out),
+        lambda out: layers.embedding_backward(ids, x, 8, out=[out]),
+        lambda out: layers.embedding_backward(ids, x, 8, out=[out], accumulate=True),
+        lambda out: layers.layer_norm_forward(x, w, out=out),
+        lambda out: layers.layer_norm_backward(x, x, w, stat, stat, out=out),
+        lambda out: layers.distill_loss_and_grad(x, ids[:, None], stat[:, None], out=out),
+    ]
+    for call in calls:
+        leaf = torch.randn(8, 16, device="cuda", requires_grad=True)
+        saved = leaf.exp()
+        with torch.no_grad():
+            call(saved)
+        assert saved._version == 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.sum().backward()
+        with torch.inference_mode():
+            plain = torch.zeros(8, 16, device="cuda")
+            call(plain)
+        call(plain)
+        assert plain.any()
+    assert x._version == 0 and w._version == 0
