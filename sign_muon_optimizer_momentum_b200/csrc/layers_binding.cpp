@@ -5,7 +5,6 @@
 // and marshalling in Python took two to four times as long as a small
 // operator's kernels.
 #include <ATen/ATen.h>
-#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -83,12 +82,39 @@ int64_t check_out(const Tensor& t, at::IntArrayRef shape, at::ScalarType dtype, 
   return rows_of(t, what).ld;
 }
 
+// A tensor's memory: n pieces of `bytes` that start `step` apart.
+struct Pieces {
+  const char* p;
+  int64_t n, bytes, step;
+};
+Pieces pieces_of(const Tensor& t) {
+  const char* p = static_cast<const char*>(t.const_data_ptr());
+  const int64_t all = (int64_t)t.nbytes(), size = (int64_t)t.element_size();
+  if (!all || t.is_contiguous()) return {p, 1, all, all};
+  const RowsOf r = rows_of(t, "tensor");
+  return {p, r.n, r.cols * size, r.ld * size};
+}
+// Whether they have bytes in common.  (Of rows of two different strides this is
+// not known: false.)
+bool overlap(Pieces a, Pieces b) {
+  if (!a.bytes || !b.bytes || a.p + (a.n - 1) * a.step + a.bytes <= b.p || b.p + (b.n - 1) * b.step + b.bytes <= a.p) return false;
+  if (a.n == 1) std::swap(a, b);
+  if (b.n == 1) {
+    // The first piece of a that ends behind b's start.
+    const int64_t before = b.p - a.p - a.bytes, k = before < 0 ? 0 : before / a.step + 1;
+    return k < a.n && a.p + k * a.step < b.p + b.bytes;
+  }
+  if (a.step != b.step) return false;
+  const int64_t off = ((b.p - a.p) % a.step + a.step) % a.step;
+  return off < a.bytes || off + b.bytes > a.step;
+}
+
 // An output shares no memory with an input; or, where that is allowed, it is
-// the same tensor.  (Of tensors with gaps between their rows this cannot be
-// told: they may be columns of one buffer.)
+// the same tensor.
 void check_apart(const Tensor& out, const Tensor& in, const char* what, bool same = false) {
-  const at::MemOverlapStatus s = at::get_overlap_status(out, in);
-  TORCH_CHECK_VALUE(s != at::MemOverlapStatus::Partial && (same || s != at::MemOverlapStatus::Full), "out overlaps ", what);
+  const Pieces a = pieces_of(out), b = pieces_of(in);
+  if (same && a.p == b.p && a.n == b.n && a.bytes == b.bytes && a.step == b.step) return;
+  TORCH_CHECK_VALUE(!overlap(a, b), "out overlaps ", what);
 }
 
 // Tells autograd that a caller's tensor has been written to: a backward pass that
@@ -354,6 +380,7 @@ PYBIND11_MODULE(_layers_native, m) {
   m.def("distill", &distill);
   // For tests.
   m.def("shares", &shares);
+  m.def("overlap", [](const Tensor& a, const Tensor& b) { return overlap(pieces_of(a), pieces_of(b)); });
   m.def("rows_of", [](const Tensor& t) {
     const RowsOf r = rows_of(t, "t");
     return std::make_tuple(r.n, r.cols, r.ld);

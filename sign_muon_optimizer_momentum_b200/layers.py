@@ -24,9 +24,11 @@ functions are called for that.
 Nothing synchronises, so every call can be captured into a CUDA graph, and
 scratch is allocated per call, so calls on different streams (and captured
 graphs) share nothing.  The gradients that a call returns for the workers are
-views of one allocation; out may not overlap an input unless stated.  Tensors are fp32 or bf16 on one CUDA device; rows may
-have any stride, columns must be adjacent.  Wrong arguments raise TypeError or
-ValueError, failures in the library SignMuonError.
+views of one allocation; out may not overlap an input unless stated (this is
+checked, but for tensors of rows with two different strides), and a write to it
+counts in its version as an in-place operation's.  Tensors are fp32 or bf16 on
+one CUDA device; rows may have any stride, columns must be adjacent.  Wrong
+arguments raise TypeError or ValueError, failures in the library SignMuonError.
 """
 from __future__ import annotations
 

@@ -315,3 +315,46 @@ def test_autograd_sees_what_is_written(cuda_lib):
         call(plain)
         assert plain.any()
     assert x._version == 0 and w._version == 0
+
+
+def test_overlap_of_row_tensors(lib):
+    """Against the sets of bytes themselves, over views of one buffer."""
+    overlap = layers._load().overlap
+    buf = torch.zeros(400)
+    where = torch.arange(400)
+    views = [(off, n, cols, ld) for off in (0, 1, 5, 17, 40, 83, 200) for n in (1, 2, 5) for cols in (1, 4, 12)
+             for ld in (12, 16, 21) if off + (n - 1) * ld + cols <= 400]
+    tensors = [buf[off:].as_strided((n, cols), (ld, 1)) for off, n, cols, ld in views]
+    bytes_of = [set(where[off:].as_strided((n, cols), (ld, 1)).flatten().tolist()) for off, n, cols, ld in views]
+    for (va, a, sa) in zip(views, tensors, bytes_of):
+        for (vb, b, sb) in zip(views, tensors, bytes_of):
+            known = va[3] == vb[3] or a.is_contiguous() or b.is_contiguous() or va[1] == 1 or vb[1] == 1
+            if known:
+                assert overlap(a, b) == bool(sa & sb), (va, vb)
+            else:
+                assert not overlap(a, b) or sa & sb
+    assert not overlap(buf[:0], buf) and not overlap(buf, torch.zeros(400))
+
+
+@pytest.mark.gpu
+def test_rows_that_overlap_are_refused(cuda_lib):
+    """Outputs whose rows lie partly over an input's rows; columns of one buffer
+    that do not are taken."""
+    buf = torch.randn(8, 40, device="cuda")
+    w, stat, ids = torch.ones(16, device="cuda"), torch.ones(8, device="cuda"), torch.arange(8, device="cuda")
+    x, over, beside = buf[:, :16], buf[:, 8:24], buf[:, 16:32]
+    calls = [
+        lambda out: layers.embedding_forward(x, ids, out=out),
+        lambda out: layers.layer_norm_forward(x, w, out=out)[0],
+        lambda out: layers.layer_norm_backward(x, x.clone(), w, stat, stat, out=out)[0],
+        lambda out: layers.layer_norm_backward(x.clone(), x, w, stat, stat, out=out)[0],
+        lambda out: layers.distill_loss_and_grad(x, ids[:, None], stat[:, None], out=out)[2],
+    ]
+    for call in calls:
+        kept = buf.clone()
+        for bad in (over, buf[:, 1:17], torch.as_strided(buf, (8, 16), (40, 1), 5)):
+            with pytest.raises(ValueError, match="overlap"):
+                call(bad)
+        assert torch.equal(buf, kept)
+        want = call(torch.empty(8, 16, device="cuda"))
+        assert torch.equal(call(beside), want) and torch.equal(buf[:, :16], kept[:, :16]) and torch.equal(buf[:, 32:], kept[:, 32:])
