@@ -3,6 +3,9 @@ temperatures, buffers that a caller owns, sizes where a cost could run away.
 
 Bounds as in test_layers: U = 2^-24 is the most an fp32 rounding is off,
 `half` the same for an output's type."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -358,3 +361,38 @@ def test_rows_that_overlap_are_refused(cuda_lib):
         assert torch.equal(buf, kept)
         want = call(torch.empty(8, 16, device="cuda"))
         assert torch.equal(call(beside), want) and torch.equal(buf[:, :16], kept[:, :16]) and torch.equal(buf[:, 32:], kept[:, 32:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_readme_training_example(cuda_lib, dtype):
+    """The README's passes over a tied table, run as they stand there, against
+    autograd on each worker's rows."""
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        code, = (c for c in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "embedding_backward" in c)
+    workers, rows, vocab, d, top = 8, 128, 160, 64, 6
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+
+    def normal(*shape, std=1.0, mean=0.0):
+        return (torch.randn(shape, generator=g, device="cuda") * std + mean).to(dtype)
+    table, w, b = normal(vocab, d, std=0.5), normal(d, std=0.1, mean=1.0), normal(d, std=0.1)
+    ids = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    top_ids = torch.rand(rows, vocab, generator=g, device="cuda").topk(top, dim=1).indices
+    top_logits = torch.randn(rows, top, generator=g, device="cuda")
+    here = dict(table=table, w=w, b=b, ids=ids, top_ids=top_ids, top_logits=top_logits)
+    exec(code, here)
+    t, per = 2.0, rows // workers
+    # Six roundings to the type on the way, each amplified by the sums in between by at most sqrt(d).
+    tol = 6 * d ** 0.5 * half(dtype) + 1e-5
+    for m in range(workers):
+        at = slice(m * per, (m + 1) * per)
+        T, W, B = (q.double().requires_grad_() for q in (table, w, b))
+        Y = torch.nn.functional.layer_norm(T[ids[at]], (d,), W, B, 1e-5)
+        logp = torch.log_softmax(top_logits[at].double() / t, 1)
+        logq = torch.log_softmax(Y @ T.t() / t, 1).gather(1, top_ids[at])
+        ref = (logp.exp() * (logp - logq)).sum() * t * t / per
+        ref.backward()
+        assert abs(here["loss"][m].item() - ref.item()) <= tol * abs(ref.item())
+        for got, want in ((here["d_table"][m], T.grad), (here["dw"][m], W.grad), (here["db"][m], B.grad)):
+            assert (got.double() - want).norm() <= tol * want.norm()
