@@ -11,7 +11,7 @@ import torch
 
 from sign_muon_optimizer_momentum_b200 import _lib as L
 from sign_muon_optimizer_momentum_b200 import layers
-from test_layers import BF16, F32, U, distill_inputs, distill_reference, half, lib, padded  # noqa: F401
+from test_layers import BF16, DISTILL, F32, U, distill_inputs, distill_reference, half, lib, padded  # noqa: F401
 
 
 def device_ms(f, reps=5):
@@ -396,3 +396,94 @@ def test_readme_training_example(cuda_lib, dtype):
         assert abs(here["loss"][m].item() - ref.item()) <= tol * abs(ref.item())
         for got, want in ((here["d_table"][m], T.grad), (here["dw"][m], W.grad), (here["db"][m], B.grad)):
             assert (got.double() - want).norm() <= tol * want.norm()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,top_dtype", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("shares,vocab,top,kind,extra", DISTILL)
+@pytest.mark.parametrize("temperature", [0.5, 4.0])
+def test_distill_gradient_in_place_and_at_other_addresses(cuda_lib, dtype, top_dtype, shares, vocab, top, kind, extra,
+                                                          temperature):
+    """The gradient over the logits, and into rows that lie differently within
+    16 bytes, with losses: each within the bounds of the call that has a buffer
+    of its own."""
+    z, ids, u, splits = distill_inputs(shares, vocab, top, dtype, kind, seed=1, extra=extra, top_dtype=top_dtype,
+                                       ids_dtype=torch.int64 if top % 2 else torch.int32)
+    n, t = len(shares), temperature
+    ref = distill_reference(z, ids, u, splits, t)
+    bounds = distill_bounds(z, u, splits, t, top, ref)
+    for out in (padded(torch.zeros(z.shape, dtype=dtype, device="cuda"), 3, offset=1), z):
+        got = layers.distill_loss_and_grad(z, ids, u, n, splits, temperature=t, out=out)
+        assert got[2] is out
+        check_result(got, ref, bounds)
+        dead = ~ref[5]
+        assert not got[1][dead].any() and not out[dead].any()
+
+
+def norm_reference(x, w, b, eps):
+    """y, mean, 1 / std and what each may be off, as in test_layer_norm_forward."""
+    X, W = x.double(), w.double()
+    mu = X.mean(1)
+    r = ((X - mu[:, None]).square().mean(1) + eps).rsqrt()
+    depth = 64 + x.shape[1] / 512
+    e_mu = depth * U * X.abs().mean(1) + U * mu.abs()
+    e_r = (depth + 8) * U + 2 * e_mu * r
+    xh = (X - mu[:, None]) * r[:, None]
+    e_xh = (e_mu * r)[:, None] + (e_r[:, None] + 3 * U) * xh.abs()
+    e = e_xh * W.abs() + 2 * U * ((xh * W).abs() + b.double().abs())
+    y = xh * W + b.double()
+    return (y, mu, r), (e + half(x.dtype) * (y.abs() + e), e_mu, e_r * r)
+
+
+def norm_grad_reference(dy, x, w, mean, rstd, splits):
+    """dx, dw, db and what they may be off, as in test_layer_norm_backward."""
+    r, D = rstd.double()[:, None], dy.double()
+    xh = (x.double() - mean.double()[:, None]) * r
+    gy = D * w.double()
+    s1, s2 = gy.mean(1, keepdim=True), (gy * xh).mean(1, keepdim=True)
+    dx = r * (gy - s1 - xh * s2)
+    depth = 64 + x.shape[1] / 512
+    e1 = (depth + 2) * U * gy.abs().mean(1, keepdim=True)
+    e2 = (depth + 6) * U * (gy * xh).abs().mean(1, keepdim=True)
+    e = r * (U * gy.abs() + e1 + xh.abs() * e2 + 4 * U * (gy.abs() + s1.abs() + (xh * s2).abs()) + 2 * U * xh.abs() * s2.abs())
+    out = [(dx, e + half(x.dtype) * (dx.abs() + e))]
+    for terms in (D * xh, D):
+        for a, b in zip(splits, splits[1:]):
+            ref, e = terms[a:b].sum(0), (b - a + 12) * U * terms[a:b].abs().sum(0)
+            out.append((ref, e + half(w.dtype) * (ref.abs() + e)))
+    return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [5, 8, 13, 16, 30, 60, 125, 256, 500, 512, 768, 1000, 1024, 1500, 1536, 2048, 2100, 4096, 5001, 8192,
+                                  8200, 12288, 12300])
+@pytest.mark.parametrize("offsets", [(1, 1, 1), (0, 1, 0), (3, 3, 2)])
+def test_layer_norm_off_16_bytes(cuda_lib, dtype, cols, offsets):
+    """Every division of a row among threads, element by element: x, dy and the
+    outputs some elements past 16 bytes, and not all alike; what lies around the
+    outputs' rows stays."""
+    shares = [5, 0, 18] if cols < 2000 else [3, 4]
+    splits = [sum(shares[:i]) for i in range(len(shares) + 1)]
+    n, m = splits[-1], len(shares)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(cols)
+
+    def normal(*shape, std=1.0, mean=0.0):
+        return (torch.randn(shape, generator=g, device="cuda") * std + mean).to(dtype)
+
+    def lay(t, i):
+        return padded(t, offsets[i] + 2, offset=offsets[i])
+    x, dy = lay(normal(n, cols, std=2.0, mean=1.0), 0), lay(normal(n, cols), 1)
+    w, b = normal(cols, std=0.2, mean=1.0), normal(cols)
+    y = lay(torch.zeros(n, cols, dtype=dtype, device="cuda"), 2)
+    got = layers.layer_norm_forward(x, w, b, out=y)
+    for a, ref, e in zip(got, *norm_reference(x, w, b, 1e-5)):
+        assert ((a.double() - ref).abs() <= e).all()
+    dx = lay(torch.zeros(n, cols, dtype=dtype, device="cuda"), 2)
+    ref = norm_grad_reference(dy, x, w, got[1], got[2], splits)
+    got = layers.layer_norm_backward(dy, x, w, got[1], got[2], m, splits, out=dx)
+    for a, (r, e) in zip((got[0], *got[1], *got[2]), ref):
+        assert ((a.double() - r).abs() <= e).all()
+    for out in (y, dx):
+        assert out._base.isnan().sum() == n * (offsets[2] + 2)
