@@ -487,3 +487,48 @@ def test_layer_norm_off_16_bytes(cuda_lib, dtype, cols, offsets):
         assert ((a.double() - r).abs() <= e).all()
     for out in (y, dx):
         assert out._base.isnan().sum() == n * (offsets[2] + 2)
+
+
+@pytest.mark.gpu
+def test_rows_beyond_two_to_the_31_elements(cuda_lib):
+    """The last rows of buffers of more than 2^31 elements, against calls on
+    those rows alone."""
+    n, cols, last = 540000, 4096, 700
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    assert (n - last) * cols > 1 << 31
+    table = torch.randn(n, cols, generator=g, device="cuda", dtype=BF16)
+    ids = torch.randperm(n, generator=g, device="cuda")
+    y = layers.embedding_forward(table, ids)
+    assert torch.equal(y[-last:], table[ids[-last:]]) and torch.equal(y[:last], table[ids[:last]])
+    grad, = layers.embedding_backward(ids, y, n)          # every id once: the table again
+    assert torch.equal(grad, table)
+    del grad, y
+    w = torch.randn(cols, generator=g, device="cuda")
+    y, mean, rstd = layers.layer_norm_forward(table, w, out=table)
+    assert y is table
+    x = torch.randn(n, cols, generator=g, device="cuda", dtype=BF16)
+    y, mean, rstd = layers.layer_norm_forward(x, w)
+    for a, b in zip((y, mean, rstd), layers.layer_norm_forward(x[-last:], w)):
+        assert torch.equal(a[-last:], b)
+    del y
+    dx, dw, db = layers.layer_norm_backward(table, x, w, mean, rstd, 2, [0, n - last, n])
+    few = layers.layer_norm_backward(table[-last:], x[-last:], w, mean[-last:], rstd[-last:])
+    assert torch.equal(dx[-last:], few[0])
+    D = table[-last:].double()
+    xh = (x[-last:].double() - mean[-last:, None].double()) * rstd[-last:, None].double()
+    for got, terms in ((dw[1], D * xh), (db[1], D)):
+        # Sums of `last` terms, in whatever blocks.
+        assert ((got.double() - terms.sum(0)).abs() <= (last + 16) * U * terms.abs().sum(0) + U * terms.sum(0).abs()).all()
+    del table, dx, x, D, xh
+    n, vocab = 44000, 50008
+    assert (n - last) * vocab > 1 << 31
+    z = torch.randn(n, vocab, generator=g, device="cuda", dtype=BF16)
+    z[-last // 2] = -1e30                                  # one that fp64 has
+    top_ids, u = torch.randint(0, vocab, (n, 5), generator=g, device="cuda"), torch.randn(n, 5, generator=g, device="cuda")
+    few = layers.distill_loss_and_grad(z[-last:].contiguous(), top_ids[-last:].contiguous(), u[-last:].contiguous())
+    _, row, dz = layers.distill_loss_and_grad(z, top_ids, u, 2, [0, n - last, n], out=z)
+    assert ((row[-last:] - few[1]).abs() <= 128 * U * (1 + few[1].abs())).all()
+    # The same rows by other numbers of threads: sums of at most 128 terms in fp32, and bf16's roundings.
+    a, b = dz[-last:].double(), few[2].double()
+    assert ((a - b).abs() <= (128 * U + 2.0 ** -7) * b.abs() + 2.0 ** -126).all()
