@@ -349,9 +349,11 @@ signmuon_status signmuon_momentum_norm_noalloc(const signmuon_shape* shapes, int
  * workspace has to be 256-byte aligned.  Rows of embeddings and layer norms
  * have at most 2^20 columns (else SIGNMUON_ERR_UNSUPPORTED).  rows = 0 is
  * allowed (row pointers may then be NULL).  None of these kernels waits on a
- * flag in memory: no error word is recorded in the workspace.  Sums are taken in fp32 in an order fixed by the shapes and
- * ids, and rounded once, to nearest, to the output's type: results are
- * bit-reproducible.  Outputs must not overlap inputs unless stated.
+ * flag in memory: no error word is recorded in the workspace.  Sums are taken
+ * in fp32 (or fp64), without float atomics, in an order that the device, the
+ * shapes, the ids, the strides and the buffers' places within 16 bytes fix: the
+ * same call gives the same bits.  What they come to is rounded to nearest to
+ * the output's type.  Outputs must not overlap inputs unless stated.
  * ---------------------------------------------------------------------- */
 
 /* Embedding lookup: y[t, :] = scale * table[ids[t], :], zero where ids[t] is
@@ -367,9 +369,10 @@ signmuon_status signmuon_embedding_forward(signmuon_shape table_shape, signmuon_
  *   grad[m][v, :] = scale * sum over worker m's tokens t with ids[t] == v of dy[t, :]
  * (accumulate == 0: every row is written, zero where no token names it), or
  * that sum added to grad[m][v, :] (accumulate != 0: only rows that a token
- * names are touched; one rounding of old + sum).  Tokens outside the table
- * give nothing.  Each worker's tokens are sorted by id and added in token
- * order.
+ * names are touched; old + scale * sum is one fused operation in fp32, and
+ * rounded to the type).  Tokens outside the table give nothing.  Each worker's
+ * tokens are sorted by id; a row's terms are added in chunks of consecutive
+ * tokens, and the chunks' sums after them.
  * dy: device [row_begin[n_workers], ld_dy] of dy_dtype; grad: host array of
  * n_workers device pointers, [rows, cols] of grad_dtype, row stride cols; no
  * two of them overlap.  At most 2^30 tokens (else SIGNMUON_ERR_UNSUPPORTED).

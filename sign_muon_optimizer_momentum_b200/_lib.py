@@ -267,9 +267,8 @@ def signmuon_momentum_norm_noalloc(shapes, n_workers, grad_dtype, grad, mom, bet
 
 
 def _offsets(row_begin):
-    """Row offsets (a sequence, or an int64 array made by an earlier call) as
-    a C array; its length is the number of workers + 1."""
-    return row_begin if isinstance(row_begin, ctypes.Array) else (ctypes.c_int64 * len(row_begin))(*row_begin)
+    """Row offsets as a C array; its length is the number of workers + 1."""
+    return (ctypes.c_int64 * len(row_begin))(*row_begin)
 
 
 def signmuon_embedding_forward(table_shape, table_dtype, table, ld_table, n_tokens, ids_int64, ids, scale, y_dtype, y,

@@ -275,7 +275,10 @@ struct Team {
 
 // A row from its definition in fp64, differences before products, with the
 // entries as they were given.  The gradient may take the logits' place; `scale` is
-// its factor.  The row's entries in the workspace are used up.
+// its factor.  The row's entries in the workspace are used up.  Bound by the fp64
+// exponentials, one an element for the loss and one for the gradient: 2048 rows of
+// 50000 bf16, all of them left, 893 us (losses alone 533), and 8192 of 512 at a high
+// temperature 195, where fp32 does they take 107, 56 and 64.
 template <typename T, bool kGrad, bool kWarp>
 __device__ __forceinline__ void left_row(const RowArgs& a, int64_t row, double scale, double* sh) {
   using G = Team<kWarp>;
@@ -483,7 +486,7 @@ short_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, i
 // losses alone a block holds the kDepth batches that come next.
 //
 // Bound by memory and by instructions about equally: 8192 rows of 50000 bf16 with
-// their gradient in 345 us (floor 255; 289 with no exponential at all, 310 with one
+// their gradient in 349 us (floor 255; when it took 345, 289 with no exponential at all, 310 with one
 // of the two), 513 of 131101 fp32 in 117 (floor 83; the same without exponentials:
 // ten rounds of clusters for 9.3 of work).  Losses alone: 2048 rows of 50000 fp32 in
 // 68 us (floor 64).
@@ -977,7 +980,7 @@ held_rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers, in
 // within them, or a row is too long for a cluster's shared memory: the second
 // pass reads the row again.  Elements before the first and after the last
 // whole 16 bytes are taken one at a time.  (2048 rows of 50000 with their gradient,
-// one element past 16 bytes: bf16 224 us, fp32 372; on 16 bytes, held: 104 and 160.)
+// one element past 16 bytes: bf16 142 us, fp32 269; on 16 bytes, held: 107 and 163.)
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads)
 rows_kernel(const RowArgs a, const __grid_constant__ WorkerRows workers) {
